@@ -115,11 +115,11 @@ def _noise(gen, shape, dtype):
 
 def _kv4_pool(gen, pages, kv_heads):
     """Pages of K and V of unit spread in 4 bits, as the rows of earlier tokens left them."""
-    pool = torch.empty((pages, 2, kv_heads, 1152), dtype=torch.uint8, device="cuda")
+    pool = torch.empty((pages, kv_heads, 2, 1152), dtype=torch.uint8, device="cuda")
     step = max(1, 4_000_000 // (kv_heads * 4096))
     for p in range(0, pages, step):
         part = pool[p:p + step]
-        x = _noise(gen, (part.shape[0], 2, kv_heads, PAGE, HD), torch.float32) * 1.28
+        x = _noise(gen, (part.shape[0], kv_heads, 2, PAGE, HD), torch.float32) * 1.28
         codes, scales = _quantise(x, torch.float32)
         part[..., :1024] = codes.flatten(-2)
         part[..., 1024:] = scales.flatten(-2)
@@ -229,8 +229,8 @@ def _live(st):
 def _plain_attention(st):
     case = st["case"]
     B, W, hq, hkv = case["batch"], st["width"], case["heads"], case["kv_heads"]
-    kv = _dequantise(*_split(st["pool"][st["table"].clamp(min=0).long()]))   # [B, pages, 2, hkv, 16, 128]
-    kv = kv.permute(2, 0, 3, 1, 4, 5).flatten(3, 4)                           # [2, B, hkv, keys, 128]
+    kv = _dequantise(*_split(st["pool"][st["table"].clamp(min=0).long()]))   # [B, pages, hkv, 2, 16, 128]
+    kv = kv.permute(3, 0, 2, 1, 4, 5).flatten(3, 4)                           # [2, B, hkv, keys, 128]
     q = st["q"].float().unflatten(0, (B, W)).unflatten(2, (hkv, hq // hkv)).permute(0, 2, 1, 3, 4).flatten(2, 3)
     score = torch.matmul(q, kv[0].transpose(-1, -2)) * (st["k_scale"] / HD ** 0.5)
     last = st["S"][:, None] + torch.arange(W, device="cuda")[None]
@@ -249,11 +249,11 @@ def _plain_rows(st):
     codes, scales = _split(st["pool"])
     for which, name in enumerate("kv"):
         code, scale = _quantise(st[name][at].double() / st[name + "_scale"], torch.float64)
-        codes[page, which, :, token] = code
-        scales[page, which, :, token] = scale
-    rows = _dequantise(codes[page, :, :, token], scales[page, :, :, token])  # [rows, 2, hkv, 128]
-    st["out"][0][at] = (rows[:, 0] * st["k_scale"]).to(st["out"][0].dtype)
-    st["out"][1][at] = (rows[:, 1] * st["v_scale"]).to(st["out"][1].dtype)
+        codes[page, :, which, token] = code
+        scales[page, :, which, token] = scale
+    rows = _dequantise(codes[page, :, :, token], scales[page, :, :, token])  # [rows, hkv, 2, 128]
+    st["out"][0][at] = (rows[:, :, 0] * st["k_scale"]).to(st["out"][0].dtype)
+    st["out"][1][at] = (rows[:, :, 1] * st["v_scale"]).to(st["out"][1].dtype)
     return st["out"]
 
 
@@ -444,9 +444,9 @@ def exact(case, seed):
     out = torch.zeros((case["batch"] * W, hq, HD), dtype=torch.float64, device="cuda")
     for b in range(case["batch"]):
         keys = S[b] + n[b]
-        kv = _values64(st["pool"][st["table"][b, :(keys + PAGE - 1) // PAGE].long()])   # [pages, 2, hkv, 16, 128]
-        K = kv[:, 0].permute(1, 0, 2, 3).reshape(hkv, -1, HD)[:, :keys] * st["k_scale"]
-        V = kv[:, 1].permute(1, 0, 2, 3).reshape(hkv, -1, HD)[:, :keys] * st["v_scale"]
+        kv = _values64(st["pool"][st["table"][b, :(keys + PAGE - 1) // PAGE].long()])   # [pages, hkv, 2, 16, 128]
+        K = kv[:, :, 0].permute(1, 0, 2, 3).reshape(hkv, -1, HD)[:, :keys] * st["k_scale"]
+        V = kv[:, :, 1].permute(1, 0, 2, 3).reshape(hkv, -1, HD)[:, :keys] * st["v_scale"]
         q = st["q"][b * W:b * W + n[b]].double()
         for h in range(hq):
             z = q[:, h] @ K[h * hkv // hq].T / HD ** 0.5
