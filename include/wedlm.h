@@ -476,6 +476,133 @@ wedlm_status wedlm_attention_bf16(const void* q, const void* kv_pool, int32_t nu
                                   int32_t max_ctx, void* out, void* workspace, int64_t workspace_bytes,
                                   void* stream);
 
+/* A KV cache held in 4 bits.  A row of 128 dims (K or V of one token and head)
+ * is 8 blocks of 16 dims; a block x is stored as one e4m3 scale
+ *   s = e4m3(max|x / g| / 6)          (to nearest even, at most 448)
+ * and 16 e2m1 codes
+ *   c_i = e2m1(x_i / (g s))           (to nearest even; +-{0, .5, 1, 1.5, 2, 3, 4, 6}),
+ * and stands for c_i s g, where g is the call's k_scale or v_scale: a power of
+ * two between 2^-59 and 2^58 (anything else: WEDLM_ERR_INVALID_ARG) that the
+ * caller chooses once per cache so that block maxima lie well inside the scale's
+ * range, 6 * 2^-9 to 6 * 448.  A block whose s is 0 is all zeros.
+ * Pool (DEVICE memory, 16-byte aligned): [num_pages][n_kv_heads][2 (K, V)]
+ * [WEDLM_KV4_HALF_PAGE bytes], a half page being codes [16 tokens][64 bytes]
+ * (dim 2i in the low nibble of byte i, dim 2i + 1 in the high one) and then
+ * scales [16 tokens][8 bytes].  page_table int32 [n_seq][pages_per_seq] as for
+ * wedlm_attention_bf16.  Memory behind a sequence's last row may hold anything.
+ *
+ * wedlm_kv4_append writes rows r < n[b] of each sequence b to its positions
+ * S[b] + r; wedlm_kv4_read copies them back out, widened.
+ *   k, v       DEVICE [n_seq * stride] rows of [n_kv_heads][128] in `dtype`
+ *              (WEDLM_DTYPE_F32 or WEDLM_DTYPE_BF16; others:
+ *              WEDLM_ERR_UNSUPPORTED), row b * stride + r, k_stride / v_stride
+ *              elements from one row to the next (at least n_kv_heads * 128, so
+ *              columns of a fused projection can be given); pointers 16-byte
+ *              aligned and strides multiples of 16 bytes.  K after RoPE.
+ *   S, n       DEVICE int32 [n_seq].  Rows r >= n[b] are not touched.
+ *   error_word DEVICE int32, set and never cleared by the calls (the first word
+ *              of a wedlm_attention_kv4 workspace may serve): 1 a position
+ *              outside the page table or a page id outside [0, num_pages), the
+ *              row is skipped; 3 (append) a block holds a NaN or an infinity, it
+ *              is stored as zeros.
+ * Values read back are exact in both types.  Sequences that write must not
+ * share the pages they write.  Asynchronous on `stream`; no allocation. */
+#define WEDLM_KV4_HALF_PAGE 1152
+wedlm_status wedlm_kv4_append(const void* k, const void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
+                              void* kv4_pool, int32_t num_pages, int32_t n_kv_heads, const int32_t* page_table,
+                              int32_t pages_per_seq, const int32_t* S, const int32_t* n, int32_t n_seq,
+                              int32_t stride, float k_scale, float v_scale, void* error_word, void* stream);
+wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_kv_heads, const int32_t* page_table,
+                            int32_t pages_per_seq, const int32_t* S, const int32_t* n, int32_t n_seq, int32_t stride,
+                            float k_scale, float v_scale, void* k, void* v, int32_t dtype, int64_t k_stride,
+                            int64_t v_stride, void* error_word, void* stream);
+
+/* wedlm_attention_bf16 over a 4-bit cache: the same q, S, n, out and rules
+ * (rows r < n[b] see positions 0 .. S[b] + r; their own K/V must have been
+ * appended; rows r >= n[b] are not written; stride <= 1024), with pointers
+ * 16-byte aligned and the workspace 256-byte aligned, from
+ * wedlm_attention_kv4_workspace_bytes.  The workspace's first int32 is the
+ * device error word: zero it once, calls only ever set it (1: a page id outside
+ * [0, num_pages), whose 16 keys are then left out, or S[b] + n[b] > max_ctx or
+ * S[b] < 0, whose rows are not written; 2: a bounded wait gave up).  The cache
+ * enters the products unrounded; q and the softmax weights are rounded to 11
+ * significant bits, sums are fp32.  Results do not depend on other sequences.
+ * Asynchronous on `stream`; no allocation.  Calls that may overlap need a
+ * workspace each. */
+wedlm_status wedlm_attention_kv4_workspace_bytes(int32_t n_seq, int32_t stride, int32_t n_heads, int32_t n_kv_heads,
+                                                 int32_t max_ctx, int64_t* bytes);
+wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t num_pages, int32_t n_heads,
+                                 int32_t n_kv_heads, const int32_t* page_table, int32_t pages_per_seq,
+                                 const int32_t* S, const int32_t* n, int32_t n_seq, int32_t stride, int32_t max_ctx,
+                                 float k_scale, float v_scale, void* out, void* workspace, int64_t workspace_bytes,
+                                 void* stream);
+
+/* Pages of a cache that the caller keeps on the device, of any format: who
+ * holds which page, and operations on them.  All pointers are DEVICE memory.
+ *   pool         [n_layers] layers, layer_stride bytes apart, of [num_pages]
+ *                pages of page_bytes (both multiples of 16, pool 16-byte
+ *                aligned; layers must not overlap).
+ *   page_table   int32 [n_seq][pages_per_seq]: a sequence's pages, -1 behind
+ *                the last one (the table of wedlm_attention_bf16 / _kv4).
+ *   S            int32 [n_seq]: committed tokens (0: an empty sequence).
+ *   refs         int32 [num_pages], 16-byte aligned: sequences that hold the
+ *                page; 0 = free. */
+typedef struct wedlm_kv_pages {
+    void*    pool;
+    int64_t  layer_stride;
+    int64_t  page_bytes;
+    int32_t* page_table;
+    int32_t* S;
+    int32_t* refs;
+    int32_t  n_layers;
+    int32_t  num_pages;
+    int32_t  n_seq;
+    int32_t  pages_per_seq;
+} wedlm_kv_pages;
+
+/* The struct is read during the call.  Lists are DEVICE int32 [n].  workspace:
+ * 256-byte aligned, wedlm_kv_pages_workspace_bytes(num_pages, n_seq) bytes; its
+ * first int32 is the device error word: zero it once, calls only ever set it (1:
+ * an entry that breaks a rule below, which is skipped; 4: too few free pages,
+ * the call changes nothing).  Results do not depend on how threads run: free
+ * pages are taken lowest id first and handed out in list order.  Asynchronous
+ * on `stream`; no allocation, no host synchronisation, so calls can be captured
+ * in a graph; calls on one set of pages must be ordered by the caller.
+ *
+ * copy     page dst[i] := page src[i] in every layer.  A page may be written by
+ *          one entry only and not be read by another: the entries that write a
+ *          page listed twice in dst, or listed in src too, are skipped (1).
+ *          n <= num_pages.
+ * reserve  sequence seqs[i] gets free pages behind its own until it has room for
+ *          tokens[i] tokens (nothing happens where it has).  Rules: seqs distinct
+ *          and in range, 0 <= tokens <= 16 * pages_per_seq, no -1 in front of a
+ *          sequence's last page.  n <= n_seq.
+ * fork     children[i], an empty sequence, becomes a copy of parents[i]: it
+ *          shares the parent's full pages and gets a free page with a copy of
+ *          the last one if that is not full, so that both can be continued.
+ *          (The parent's pages beyond its S tokens are not shared.)  Rules:
+ *          children distinct, empty and not among the parents, the pages of the
+ *          parent's S tokens present and in use.  n <= n_seq.
+ * free     the sequence's pages lose a reference, its row becomes -1 and S 0.
+ *          Listing one twice, or an empty one, is allowed.  n <= n_seq.
+ * compact  moves pages so that the u pages in use are pages 0 .. u - 1: the k-th
+ *          used page at or past u moves into the k-th free page below u.  Table
+ *          and refs follow; map (int32 [num_pages], may be NULL) receives each
+ *          page's new id, -1 for one that was free.
+ * WEDLM_ERR_INVALID_ARG for bad sizes, alignments, pointers or a too small
+ * workspace, WEDLM_ERR_CUDA if a launch fails. */
+wedlm_status wedlm_kv_pages_workspace_bytes(int32_t num_pages, int32_t n_seq, int64_t* bytes);
+wedlm_status wedlm_kv_pages_copy(const wedlm_kv_pages* pages, const int32_t* src, const int32_t* dst, int32_t n,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+wedlm_status wedlm_kv_pages_reserve(const wedlm_kv_pages* pages, const int32_t* seqs, const int32_t* tokens, int32_t n,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+wedlm_status wedlm_kv_pages_fork(const wedlm_kv_pages* pages, const int32_t* parents, const int32_t* children,
+                                 int32_t n, void* workspace, int64_t workspace_bytes, void* stream);
+wedlm_status wedlm_kv_pages_free(const wedlm_kv_pages* pages, const int32_t* seqs, int32_t n, void* workspace,
+                                 int64_t workspace_bytes, void* stream);
+wedlm_status wedlm_kv_pages_compact(const wedlm_kv_pages* pages, int32_t* map, void* workspace,
+                                    int64_t workspace_bytes, void* stream);
+
 /* Dense projection on the bf16 tensor-core path: Y = X * W^T with X bf16
  * [M][K], W bf16 [N][K] (nn.Linear layout), Y fp32 [M][N], all DEVICE
  * pointers owned by the caller (16-byte aligned; K % 8 == 0).  This is the

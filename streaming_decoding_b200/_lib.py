@@ -35,6 +35,12 @@ class SeqStats(ctypes.Structure):
                 ("committed_len", c_i32), ("end", c_i32), ("window", c_i32), ("active", c_i32)]
 
 
+class KVPagesDesc(ctypes.Structure):
+    _fields_ = [("pool", c_vp), ("layer_stride", c_i64), ("page_bytes", c_i64), ("page_table", c_vp), ("S", c_vp),
+                ("refs", c_vp), ("n_layers", c_i32), ("num_pages", c_i32), ("n_seq", c_i32),
+                ("pages_per_seq", c_i32)]
+
+
 def header_constants() -> dict:
     """#define WEDLM_* integer constants of include/wedlm.h."""
     out = {}
@@ -90,6 +96,19 @@ _SIGS = {
     "wedlm_attention_workspace_bytes": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i64)]),
     "wedlm_attention_bf16": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32,
                                      c_vp, c_vp, c_i64, c_vp]),
+    "wedlm_kv4_append": (c_i32, [c_vp, c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32,
+                                 c_i32, c_f32, c_f32, c_vp, c_vp]),
+    "wedlm_kv4_read": (c_i32, [c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_f32, c_f32, c_vp, c_vp,
+                               c_i32, c_i64, c_i64, c_vp, c_vp]),
+    "wedlm_attention_kv4_workspace_bytes": (c_i32, [c_i32, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_i64)]),
+    "wedlm_attention_kv4": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32,
+                                    c_f32, c_f32, c_vp, c_vp, c_i64, c_vp]),
+    "wedlm_kv_pages_workspace_bytes": (c_i32, [c_i32, c_i32, ctypes.POINTER(c_i64)]),
+    "wedlm_kv_pages_copy": (c_i32, [ctypes.POINTER(KVPagesDesc), c_vp, c_vp, c_i32, c_vp, c_i64, c_vp]),
+    "wedlm_kv_pages_reserve": (c_i32, [ctypes.POINTER(KVPagesDesc), c_vp, c_vp, c_i32, c_vp, c_i64, c_vp]),
+    "wedlm_kv_pages_fork": (c_i32, [ctypes.POINTER(KVPagesDesc), c_vp, c_vp, c_i32, c_vp, c_i64, c_vp]),
+    "wedlm_kv_pages_free": (c_i32, [ctypes.POINTER(KVPagesDesc), c_vp, c_i32, c_vp, c_i64, c_vp]),
+    "wedlm_kv_pages_compact": (c_i32, [ctypes.POINTER(KVPagesDesc), c_vp, c_vp, c_i64, c_vp]),
     "wedlm_linear_bf16": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_vp]),
     "wedlm_linear_bf16_plan": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp]),
     "wedlm_linear_bf16_sched": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp]),

@@ -363,6 +363,250 @@ def attention_error(workspace) -> int:
     return int(workspace[:4].view(dtype=__import__("torch").int32)[0].item())
 
 
+# -- 4-bit KV cache and page operations --------------------------------------
+# These take torch CUDA tensors of one device (which need not be the current
+# one) and raise ValueError where a tensor's type, shape, device or layout is
+# not the documented one.  stream: a torch.cuda.Stream or a cudaStream_t handle;
+# None is torch's current stream of the tensors' device.  Results a call
+# allocates belong to that stream.
+def _want(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _on(t, device, dtype, shape, name):
+    """A contiguous tensor of the given device, dtype and shape."""
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: wants a contiguous {dtype} tensor of shape {shape} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _cuda(t, name):
+    _want(t.is_cuda, f"{name}: wants a CUDA tensor")
+    return t.device
+
+
+class _Launch:
+    """The tensors' device made current and the stream to launch on, as a context."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = torch.cuda.device(device)
+        self.handle = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        return self.handle
+
+    def __exit__(self, *a):
+        self.device.__exit__(*a)
+
+
+def _empty_on(stream, device, shape, dtype):
+    """A new tensor of the launch's stream (of the current one for a plain handle)."""
+    import torch
+    if stream is None or isinstance(stream, int):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def kv4_pool(num_pages: int, n_kv_heads: int, n_layers: int | None = None, device="cuda"):
+    """A zeroed pool of 4-bit pages: uint8 [n_layers,] num_pages, n_kv_heads, 2, WEDLM_KV4_HALF_PAGE."""
+    import torch
+    shape = (num_pages, n_kv_heads, 2, C["WEDLM_KV4_HALF_PAGE"])
+    return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _kv4_args(kv4_pool, page_table, S, n, device):
+    import torch
+    half = C["WEDLM_KV4_HALF_PAGE"]
+    _want(kv4_pool.dim() == 4 and kv4_pool.shape[2:] == (2, half), f"kv4_pool: wants [pages, kv heads, 2, {half}]")
+    _on(kv4_pool, device, torch.uint8, tuple(kv4_pool.shape), "kv4_pool")
+    _want(page_table.dim() == 2, "page_table: wants [n_seq, pages_per_seq]")
+    n_seq = page_table.shape[0]
+    _on(page_table, device, torch.int32, tuple(page_table.shape), "page_table")
+    _on(S, device, torch.int32, (n_seq,), "S")
+    _on(n, device, torch.int32, (n_seq,), "n")
+    return n_seq, kv4_pool.shape[0], kv4_pool.shape[1]
+
+
+def _rows_arg(t, rows, hkv, device, dtype, name):
+    """Rows [rows, hkv, 128] whose heads lie side by side; any row stride the library takes."""
+    if (t.dim() != 3 or tuple(t.shape) != (rows, hkv, 128) or t.device != device or t.dtype != dtype
+            or t.stride(2) != 1 or (hkv > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: wants {dtype} [{rows}, {hkv}, 128] on {device} with the heads of a row side by "
+                         f"side, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t.stride(0) if rows > 1 else hkv * 128
+
+
+def _rows_dtype(dtype):
+    import torch
+    if dtype == torch.float32:
+        return C["WEDLM_DTYPE_F32"]
+    _want(dtype == torch.bfloat16, f"rows are float32 or bfloat16, got {dtype}")
+    return C["WEDLM_DTYPE_BF16"]
+
+
+def _error_word(t, device):
+    import torch
+    _want(t.device == device and t.is_contiguous() and t.dtype in (torch.int32, torch.uint8) and
+          t.numel() * t.element_size() >= 4, "error: wants an int32 tensor or a workspace on the same device")
+
+
+def kv4_append(k, v, kv4_pool, page_table, S, n, stride: int, error, k_scale: float = 1.0, v_scale: float = 1.0,
+               stream=None):
+    """Write K/V rows into a 4-bit cache (wedlm_kv4_append).  k, v
+    [n_seq*stride, n_kv_heads, 128] float32 or bfloat16 (views with a row stride
+    are taken as they are); kv4_pool from kv4_pool(); page_table [n_seq,
+    pages_per_seq], S, n [n_seq] int32; error: an int32 tensor, or the workspace
+    of attention_kv4, whose first word records errors (attention_error)."""
+    device = _cuda(k, "k")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
+    ks = _rows_arg(k, n_seq * stride, hkv, device, k.dtype, "k")
+    vs = _rows_arg(v, n_seq * stride, hkv, device, k.dtype, "v")
+    _error_word(error, device)
+    dt = _rows_dtype(k.dtype)
+    with _Launch(device, stream) as st:
+        _check(_lib.load().wedlm_kv4_append(_ptr(k), _ptr(v), dt, ks, vs, _ptr(kv4_pool), pages, hkv, _ptr(page_table),
+                                            page_table.shape[1], _ptr(S), _ptr(n), n_seq, stride, k_scale, v_scale,
+                                            _ptr(error), st), "wedlm_kv4_append")
+
+
+def kv4_read(kv4_pool, page_table, S, n, stride: int, error, dtype=None, k_scale: float = 1.0, v_scale: float = 1.0,
+             out=None, stream=None):
+    """Rows of a 4-bit cache, widened (wedlm_kv4_read): (k, v), each
+    [n_seq*stride, n_kv_heads, 128] in dtype (bfloat16 unless given), or written
+    into out = (k, v).  Rows r >= n[b] are left as they are."""
+    import torch
+    device = _cuda(kv4_pool, "kv4_pool")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
+    if out is None:
+        shape = (n_seq * stride, hkv, 128)
+        out = tuple(_empty_on(stream, device, shape, dtype or torch.bfloat16) for _ in range(2))
+    k, v = out
+    _want(dtype is None or k.dtype == dtype, "out and dtype disagree")
+    ks = _rows_arg(k, n_seq * stride, hkv, device, k.dtype, "k")
+    vs = _rows_arg(v, n_seq * stride, hkv, device, k.dtype, "v")
+    _error_word(error, device)
+    dt = _rows_dtype(k.dtype)
+    with _Launch(device, stream) as st:
+        _check(_lib.load().wedlm_kv4_read(_ptr(kv4_pool), pages, hkv, _ptr(page_table), page_table.shape[1], _ptr(S),
+                                          _ptr(n), n_seq, stride, k_scale, v_scale, _ptr(k), _ptr(v), dt, ks, vs,
+                                          _ptr(error), st), "wedlm_kv4_read")
+    return k, v
+
+
+def attention_kv4_workspace(n_seq: int, stride: int, n_heads: int, n_kv_heads: int, max_ctx: int, device="cuda"):
+    """A zeroed workspace for attention_kv4 (uint8 CUDA tensor)."""
+    import torch
+    nb = ctypes.c_int64()
+    with torch.cuda.device(torch.device(device)):
+        _check(_lib.load().wedlm_attention_kv4_workspace_bytes(n_seq, stride, n_heads, n_kv_heads, max_ctx,
+                                                               ctypes.byref(nb)), "wedlm_attention_kv4_workspace_bytes")
+        return torch.zeros(int(nb.value), dtype=torch.uint8, device=device)
+
+
+def attention_kv4(q, kv4_pool, page_table, S, n, stride: int, n_heads: int, n_kv_heads: int, max_ctx: int, workspace,
+                  k_scale: float = 1.0, v_scale: float = 1.0, out=None, stream=None):
+    """attention_bf16 over a 4-bit cache (wedlm_attention_kv4).  q and out
+    [n_seq*stride, n_heads, 128] bfloat16; the cache arguments as in kv4_append;
+    workspace from attention_kv4_workspace() with the same sizes.  Returns `out`;
+    read attention_error(workspace) after synchronising."""
+    import torch
+    device = _cuda(q, "q")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
+    _want(hkv == n_kv_heads, "kv4_pool has another number of KV heads")
+    shape = (n_seq * stride, n_heads, 128)
+    _on(q, device, torch.bfloat16, shape, "q")
+    if out is None:
+        out = _empty_on(stream, device, shape, torch.bfloat16)
+    else:
+        _on(out, device, torch.bfloat16, shape, "out")
+    _on(workspace, device, torch.uint8, tuple(workspace.shape), "workspace")
+    with _Launch(device, stream) as st:
+        _check(_lib.load().wedlm_attention_kv4(_ptr(q), _ptr(kv4_pool), pages, n_heads, hkv, _ptr(page_table),
+                                               page_table.shape[1], _ptr(S), _ptr(n), n_seq, stride, max_ctx, k_scale,
+                                               v_scale, _ptr(out), _ptr(workspace), workspace.numel(), st),
+               "wedlm_attention_kv4")
+    return out
+
+
+class KVPages:
+    """Pages of a cache kept on the device, and the operations on them
+    (wedlm_kv_pages_*): all asynchronous, without a host round trip.
+
+    pool [n_layers, num_pages, ...] of any type, each page contiguous and pages
+    side by side (layers may lie further apart); page_table [n_seq,
+    pages_per_seq] (-1 behind a sequence's pages), S [n_seq] (committed tokens)
+    and refs [num_pages] (sequences holding a page; 0 = free), int32.  The
+    tensors are used in place and stay the caller's.  Lists are int32 tensors."""
+
+    def __init__(self, pool, page_table, S, refs, workspace=None):
+        import torch
+        self.device = device = _cuda(pool, "pool")
+        _want(pool.dim() >= 3 and pool[0].is_contiguous(), "pool: wants [n_layers, num_pages, ...] with contiguous layers")
+        layers, pages = pool.shape[:2]
+        _want(page_table.dim() == 2, "page_table: wants [n_seq, pages_per_seq]")
+        n_seq = page_table.shape[0]
+        _on(page_table, device, torch.int32, tuple(page_table.shape), "page_table")
+        _on(S, device, torch.int32, (n_seq,), "S")
+        _on(refs, device, torch.int32, (pages,), "refs")
+        nb = ctypes.c_int64()
+        _check(_lib.load().wedlm_kv_pages_workspace_bytes(pages, n_seq, ctypes.byref(nb)),
+               "wedlm_kv_pages_workspace_bytes")
+        if workspace is None:
+            workspace = torch.zeros(int(nb.value), dtype=torch.uint8, device=device)
+        _on(workspace, device, torch.uint8, tuple(workspace.shape), "workspace")
+        self.pool, self.page_table, self.S, self.refs, self.workspace = pool, page_table, S, refs, workspace
+        size = pool.element_size()
+        stride = pool.stride(0) if layers > 1 else pool[0].numel()
+        self._desc = _lib.KVPagesDesc(_ptr(pool), stride * size, pool[0, 0].numel() * size, _ptr(page_table), _ptr(S),
+                                      _ptr(refs), layers, pages, n_seq, page_table.shape[1])
+        self._by = ctypes.byref(self._desc)
+
+    def _list(self, t, name, n=None):
+        import torch
+        _on(t, self.device, torch.int32, (t.numel() if n is None else n,), name)
+        return t.numel()
+
+    def _call(self, name, stream, *args):
+        with _Launch(self.device, stream) as st:
+            _check(getattr(_lib.load(), name)(self._by, *args, _ptr(self.workspace), self.workspace.numel(), st), name)
+
+    def copy(self, src, dst, stream=None):
+        """Page dst[i] := page src[i] in every layer."""
+        n = self._list(src, "src")
+        self._list(dst, "dst", n)
+        self._call("wedlm_kv_pages_copy", stream, _ptr(src), _ptr(dst), n)
+
+    def reserve(self, seqs, tokens, stream=None):
+        """Free pages for seqs[i] until it has room for tokens[i] tokens."""
+        n = self._list(seqs, "seqs")
+        self._list(tokens, "tokens", n)
+        self._call("wedlm_kv_pages_reserve", stream, _ptr(seqs), _ptr(tokens), n)
+
+    def fork(self, parents, children, stream=None):
+        """children[i], an empty sequence, becomes a copy of parents[i] that shares its full pages."""
+        n = self._list(parents, "parents")
+        self._list(children, "children", n)
+        self._call("wedlm_kv_pages_fork", stream, _ptr(parents), _ptr(children), n)
+
+    def free(self, seqs, stream=None):
+        """Drop the sequences: their pages lose a reference, rows become -1 and S 0."""
+        self._call("wedlm_kv_pages_free", stream, _ptr(seqs), self._list(seqs, "seqs"))
+
+    def compact(self, map=None, stream=None):
+        """Move the u pages in use to ids 0 .. u - 1; map [num_pages] int32 receives the new ids."""
+        if map is not None:
+            self._list(map, "map", self.refs.numel())
+        self._call("wedlm_kv_pages_compact", stream, _ptr(map))
+
+    def error(self) -> int:
+        """The device error word (synchronise first)."""
+        return attention_error(self.workspace)
+
+
 def linear_bf16(X, W, stream=None, tile_n: int = 0, k_splits: int = 0, cta_pair: bool = False,
                 hybrid: bool = False, cluster_k: bool = False):
     """Y = X W^T (fp32) on the tcgen05 GEMM; X [M][K], W [N][K] torch.bfloat16 CUDA tensors.

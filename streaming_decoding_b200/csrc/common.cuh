@@ -50,7 +50,8 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 // Device error word codes (mirrors of the wedlm_status values they map to).
 constexpr int kErrBounds = 1;     // a bounds check refused an access
 constexpr int kErrTimeout = 2;    // a bounded wait gave up
-constexpr int kErrNonFinite = 3;  // a masked slot's logits held a NaN or an infinity
+constexpr int kErrNonFinite = 3;  // a masked slot's logits or a cached row held a NaN or an infinity
+constexpr int kErrPages = 4;      // not enough free pages: the call changed nothing
 
 __device__ __forceinline__ void set_error(int* err, int code) {
     if (err) atomicCAS(err, 0, code);

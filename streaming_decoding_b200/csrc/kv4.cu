@@ -1,0 +1,746 @@
+// A KV cache held in 4 bits and the attention that reads it.
+//
+// Format.  A row of 128 dims (one token's K or V of one head) is 8 blocks of
+// 16 dims; a block is one scale s (e4m3) and 16 codes (e2m1: +-{0, .5, 1, 1.5,
+// 2, 3, 4, 6}), and stands for code * s * k_scale (or v_scale), the latter a
+// power of two the caller chooses.  4.5 bits per value, against 16.
+//   s = e4m3(max|x| / 6),  code = e2m1(x / s),  both rounded to nearest even.
+// A code has 2 and a scale 4 significant bits, so code * s is exact in fp16
+// (at most 6 * 448, at least 2^-10): the attention multiplies them in fp16 and
+// feeds the tensor cores without any rounding.
+//
+// A page of one head is 2304 contiguous bytes: [K, V][codes: 16 tokens x 64
+// bytes (dim 2i in the low, 2i + 1 in the high nibble of byte i)][scales: 16
+// tokens x 8 bytes], brought in by one bulk copy.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda_fp16.h>
+
+#include "kernels.cuh"
+
+namespace wedlm {
+namespace {
+
+constexpr int HD = 128;
+constexpr int kHalfPage = WEDLM_KV4_HALF_PAGE;  // K or V of one head's page
+constexpr int kHeadPage = 2 * kHalfPage;  // both
+constexpr int kCodes = kPage * HD / 2;    // bytes of codes in a half page
+
+// ---------------------------------------------------------------------------
+// Conversions between fp32 / fp16 and the 4- and 8-bit formats (one
+// instruction each on sm_100a).
+// The four bytes of a word: eight values.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ uint32_t f32_to_e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, z;\n\tmov.b16 {z, z}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "mov.b32 %0, {a, z, z, z};\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xFFu;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t a) { return __half22float2(*reinterpret_cast<__half2*>(&a)); }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// ---------------------------------------------------------------------------
+// Rows in and out of the cache.
+struct RowsParams {
+    uint8_t* pool;
+    const int32_t* table;
+    const int32_t* S;
+    const int32_t* n;
+    int* err;
+    int64_t total;   // 16-dim blocks of K and V over all rows
+    int64_t k_stride, v_stride;
+    int num_pages, hkv, pages_per_seq, stride;
+    float k_scale, v_scale;
+};
+
+// Block i of a launch: (row, K or V, head, 16-dim block), the block fastest.
+struct RowBlock {
+    int64_t row;
+    int which, head, blk;
+    uint8_t* codes;  // 8 bytes
+    uint8_t* scale;
+};
+
+__device__ __forceinline__ bool locate(const RowsParams& p, int64_t i, RowBlock& o) {
+    o.blk = (int)(i & 7);
+    const int64_t j = i >> 3;
+    const int64_t jj = j / p.hkv;
+    o.head = (int)(j - jj * p.hkv);
+    o.which = (int)(jj & 1);
+    o.row = jj >> 1;
+    const int64_t b = o.row / p.stride;
+    const int r = (int)(o.row - b * p.stride);
+    if (r >= __ldcg(p.n + b)) return false;
+    const int64_t pos = (int64_t)__ldcg(p.S + b) + r;
+    if (pos < 0 || pos >= (int64_t)p.pages_per_seq * kPage || pos < r) {  // pos < r: a negative S
+        set_error(p.err, kErrBounds);
+        return false;
+    }
+    const int page = __ldcg(p.table + b * p.pages_per_seq + pos / kPage);
+    if (page < 0 || page >= p.num_pages) {
+        set_error(p.err, kErrBounds);
+        return false;
+    }
+    const int tok = (int)(pos % kPage);
+    uint8_t* half = p.pool + (((int64_t)page * p.hkv + o.head) * 2 + o.which) * kHalfPage;
+    o.codes = half + tok * 64 + o.blk * 8;
+    o.scale = half + kCodes + tok * 8 + o.blk;
+    return true;
+}
+
+__device__ __forceinline__ void load16(const float* x, float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float4 f = __ldcg(reinterpret_cast<const float4*>(x) + j);
+        v[4 * j] = f.x;
+        v[4 * j + 1] = f.y;
+        v[4 * j + 2] = f.z;
+        v[4 * j + 3] = f.w;
+    }
+}
+__device__ __forceinline__ void load16(const bf16* x, float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint4 u = __ldcg(reinterpret_cast<const uint4*>(x) + j);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+            v[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
+    }
+}
+__device__ __forceinline__ void store16(float* x, const float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        reinterpret_cast<float4*>(x)[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void store16(bf16* x, const float (&v)[16]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&t);
+        }
+        reinterpret_cast<uint4*>(x)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A thread per block of 16 dims.  max / 6 and x / s are correctly rounded fp32
+// divisions: a quotient that is halfway between two codes (or scales) is exact
+// and one that is not stays on its side, so the codes are those of the
+// definition in real arithmetic.  A block with a NaN or an infinity is stored
+// as zeros and recorded in the error word: the cache only ever holds finite
+// values.
+template <typename T>
+__global__ void __launch_bounds__(256) kv4_append_kernel(const T* k, const T* v, RowsParams p) {
+    griddep_wait();
+    griddep_launch();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    RowBlock o;
+    if (i >= p.total || !locate(p, i, o)) return;
+    float x[16];
+    load16((o.which ? v + o.row * p.v_stride : k + o.row * p.k_stride) + o.head * HD + o.blk * 16, x);
+    const float g = 1.0f / (o.which ? p.v_scale : p.k_scale);  // powers of two: exact
+    float m = 0.f, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        sum += x[j] * 0.f;  // NaN if any is not finite
+        x[j] *= g;
+        m = fmaxf(m, fabsf(x[j]));
+    }
+    uint32_t lo = 0, hi = 0, sc = 0;
+    if (sum != 0.f) {
+        set_error(p.err, kErrNonFinite);
+    } else {
+        sc = f32_to_e4m3(__fdiv_rn(fminf(m, 3.0e38f), 6.0f));
+        const float s = half2_floats(e4m3x2_to_f16x2(sc)).x;
+        if (sc) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo |= f32_to_e2m1x2(__fdiv_rn(x[2 * j], s), __fdiv_rn(x[2 * j + 1], s)) << (8 * j);
+                hi |= f32_to_e2m1x2(__fdiv_rn(x[8 + 2 * j], s), __fdiv_rn(x[9 + 2 * j], s)) << (8 * j);
+            }
+        }
+    }
+    *reinterpret_cast<uint2*>(o.codes) = make_uint2(lo, hi);
+    *o.scale = (uint8_t)sc;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p) {
+    griddep_wait();
+    griddep_launch();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    RowBlock o;
+    if (i >= p.total || !locate(p, i, o)) return;
+    const uint2 c = __ldcg(reinterpret_cast<const uint2*>(o.codes));
+    const uint32_t sc = __ldcg(o.scale);
+    const float s = half2_floats(e4m3x2_to_f16x2(sc)).x * (o.which ? p.v_scale : p.k_scale);
+    float x[16];
+    uint32_t h[4];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        e2m1x8_to_f16x2(w ? c.y : c.x, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = half2_floats(h[j]);
+            x[8 * w + 2 * j] = f.x * s;
+            x[8 * w + 2 * j + 1] = f.y * s;
+        }
+    }
+    store16((o.which ? v + o.row * p.v_stride : k + o.row * p.k_stride) + o.head * HD + o.blk * 16, x);
+}
+
+// ---------------------------------------------------------------------------
+// Attention over the 4-bit cache: out = softmax(q K^T / sqrt(128)) V of window
+// rows r over cache positions 0 .. S + r, as wedlm_attention_bf16.
+//
+// Work item (a CTA of four warps): 16 query rows (window rows x the g heads
+// that share a KV head), one KV head, one chunk of keys; the warps take the
+// chunk's pages in turn, each with its own ring of page buffers filled by bulk
+// copies, and join their results at the end.  Codes go from shared memory to
+// registers, are widened and scaled there and feed mma.sync directly: no
+// widened copy of K or V is ever written anywhere.  For this the dims are
+// permuted inside the products (which changes no sum): in q K^T the lanes of a
+// quad own 32 consecutive dims each, so a lane's operands of a key are 16
+// consecutive bytes; in P V a lane owns the 16 dims of one scale block.
+//
+// Q is held in fp16 scaled per row by a power of two (its largest element in
+// [2^14, 2^15)), which keeps every bit of a bf16 q that is within 2^-28 of the
+// row's largest; the factor is undone in the fp32 scores.  P is fp16, relative
+// to a running maximum that is only raised when a score exceeds it by 2^8, and
+// times 2^6, so weights down to 2^-30 of the largest are kept; sums and
+// outputs are fp32.
+constexpr int kWarps = 4;
+constexpr int kStages = 4;
+constexpr int kRows = 16;
+constexpr int kMaxSplits = 32;
+constexpr int kMaxChunk = 2048;       // keys of a chunk, unless the context needs more per chunk
+constexpr float kLazyLog2 = 8.0f;     // growth of the maximum tolerated before O is rescaled
+constexpr float kWeightLog2 = 6.0f;   // weights are held times 2^6
+
+struct AttnKv4Params {
+    const bf16* q;
+    const uint8_t* pool;
+    const int32_t* table;
+    const int32_t* S;
+    const int32_t* n;
+    bf16* out;
+    float* part_o;    // [rows][hq][max_splits][128]
+    float2* part_ml;  // [rows][hq][max_splits]
+    int* err;
+    int num_pages, hq, hkv, pages_per_seq, n_seq, stride, max_ctx, chunk, max_splits, tiles;
+    float k_scale, v_scale;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void bar_init(uint64_t* bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bar)) : "memory");
+}
+// One head's page into shared memory; completes on `bar`.
+__device__ __forceinline__ void load_page(void* dst, const uint8_t* src, uint64_t* bar) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kHeadPage)
+                 : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(kHeadPage), "r"(smem_u32(bar)) : "memory");
+}
+
+// Key chunks of the 16-row tile that starts at query row q0.
+__device__ __forceinline__ int tile_end(int S, int rows, int q0, int g) { return S + (min(q0 + kRows, rows) - 1) / g + 1; }
+
+// A thread's 32 dims of one query row (32 c .. 32 c + 31), scaled to fp16: the
+// A operands of the 8 k-steps (two registers per step); returns the exponent
+// that was added.
+__device__ __forceinline__ int load_q(const bf16* q, bool live, uint32_t (&a)[16]) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 u = live ? __ldcg(reinterpret_cast<const uint4*>(q) + j) : make_uint4(0, 0, 0, 0);
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+    }
+    uint32_t m = 0;  // the largest magnitude's bits
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int e = m ? min(100, 14 + 127 - (int)(m >> 7)) : 0;
+    const float f = __int_as_float((e + 127) << 23);
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        a[j] = pack_half2(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
+    return e;
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4Params p) {
+    __shared__ __align__(128) uint8_t ring[kWarps][kStages][kHeadPage];
+    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+    __shared__ float2 s_ml[kWarps][kRows];
+    griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, j8 = lane >> 2;
+    const int g = p.hq / p.hkv;
+    int64_t id = blockIdx.x;
+    const int tile = (int)(id % p.tiles);
+    id /= p.tiles;
+    const int sp = (int)(id % p.max_splits);
+    id /= p.max_splits;
+    const int h = (int)(id % p.hkv), b = (int)(id / p.hkv);
+    const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
+    const int rows = n * g, q0 = tile * kRows;
+    if (n <= 0 || q0 >= rows) return;
+    if (S < 0 || (int64_t)S + n > p.max_ctx) {
+        if (threadIdx.x == 0) set_error(p.err, kErrBounds);
+        return;
+    }
+    const int kend = tile_end(S, rows, q0, g);
+    const int nsplit = (kend + p.chunk - 1) / p.chunk;
+    if (sp >= nsplit) return;
+    const int ks = sp * p.chunk, ke = min(kend, ks + p.chunk);
+    const int page0 = ks / kPage, npages = (ke + kPage - 1) / kPage - page0;
+    const int mine = npages > warp ? (npages - warp + kWarps - 1) / kWarps : 0;  // pages of this warp
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) bar_init(&bars[warp][s]);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
+    // Page ids of this warp's pages, 32 at a time, one per lane (-1: none).
+    int ids = -1;
+    auto fetch_ids = [&](int first) {
+        const int k = first + lane;
+        ids = -1;
+        if (k < mine) {
+            const int idx = page0 + warp + k * kWarps;
+            ids = idx < p.pages_per_seq ? __ldcg(table + idx) : -1;
+            if (ids < 0 || ids >= p.num_pages) {
+                set_error(p.err, kErrBounds);
+                ids = -1;
+            }
+        }
+    };
+    // Load k of this warp into its stage; a page outside the pool is not loaded
+    // and its keys count as masked.
+    uint32_t have = 0;  // bit s: the page in stage s was loaded
+    int issued = 0;
+    auto issue = [&]() {
+        if ((issued & 31) == 0) fetch_ids(issued);
+        const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
+        const int s = issued % kStages;
+        have &= ~(1u << s);
+        if (page >= 0) {
+            have |= 1u << s;
+            if (lane == 0)
+                load_page(ring[warp][s], p.pool + ((int64_t)page * p.hkv + h) * kHeadPage, &bars[warp][s]);
+        }
+        ++issued;
+    };
+    while (issued < min(mine, kStages)) issue();
+
+    // Q of rows j8 and j8 + 8 of the tile
+    uint32_t qa[16], qb[16];
+    const int ra = q0 + j8, rb = ra + 8;
+    const int64_t row0 = (int64_t)b * p.stride;
+    auto q_at = [&](int r) { return p.q + ((row0 + r / g) * p.hq + h * g + r % g) * HD + 32 * c; };
+    const int ea = load_q(q_at(min(ra, rows - 1)), ra < rows, qa);
+    const int eb = load_q(q_at(min(rb, rows - 1)), rb < rows, qb);
+    const float base = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale;
+    const float sla = base * __int_as_float((127 - ea) << 23), slb = base * __int_as_float((127 - eb) << 23);
+    const int lima = min(S + min(ra, rows - 1) / g, ke - 1), limb = min(S + min(rb, rows - 1) / g, ke - 1);
+
+    float o[16][4] = {};
+    float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // maxima in the exp2 domain
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int k = 0; k < mine; ++k) {
+        const int s = k % kStages;
+        if ((have >> s) & 1) {
+            ok = mbar_wait_bounded(smem_u32(&bars[warp][s]), (phase >> s) & 1, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            phase ^= 1u << s;
+            const uint8_t* K = ring[warp][s];
+            const uint8_t* V = K + kHalfPage;
+            const int key0 = (page0 + warp + k * kWarps) * kPage;
+            // scores of the page's 16 keys (two n-tiles of 8)
+            float sc[2][4] = {};
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tok = t * 8 + j8;
+                const uint4 u = *reinterpret_cast<const uint4*>(K + tok * 64 + c * 16);
+                const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + tok * 8 + c * 2));
+                const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t f[4];
+                    e2m1x8_to_f16x2(w[x], f);
+                    const uint32_t sx = x < 2 ? slo : shi;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int st = 2 * x + y;
+                        const uint32_t a[4] = {qa[2 * st], qb[2 * st], qa[2 * st + 1], qb[2 * st + 1]};
+                        mma_f16(sc[t], a, hmul2(f[2 * y], sx), hmul2(f[2 * y + 1], sx));
+                    }
+                }
+            }
+            const int lim_min = min(lima, limb);
+            const bool edge = __any_sync(0xffffffffu, key0 + kPage - 1 > lim_min);
+            float pa[4], pb[4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    pa[2 * t + x] = sc[t][x] * sla;
+                    pb[2 * t + x] = sc[t][2 + x] * slb;
+                }
+            if (edge) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int key = key0 + t * 8 + 2 * c + x;
+                        if (key > lima) pa[2 * t + x] = -INFINITY;
+                        if (key > limb) pb[2 * t + x] = -INFINITY;
+                    }
+            }
+            float na = fmaxf(fmaxf(pa[0], pa[1]), fmaxf(pa[2], pa[3]));
+            float nb = fmaxf(fmaxf(pb[0], pb[1]), fmaxf(pb[2], pb[3]));
+            if (__any_sync(0xffffffffu, na > ma + kLazyLog2 || nb > mb + kLazyLog2)) {
+                na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, 1));
+                na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, 2));
+                nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 1));
+                nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 2));
+                const float fa = na > ma ? exp2_fast(ma - na) : 1.f, fb = nb > mb ? exp2_fast(mb - nb) : 1.f;
+                ma = fmaxf(ma, na);
+                mb = fmaxf(mb, nb);
+                la *= fa;
+                lb *= fb;
+#pragma unroll
+                for (int t = 0; t < 16; ++t) {
+                    o[t][0] *= fa;
+                    o[t][1] *= fa;
+                    o[t][2] *= fb;
+                    o[t][3] *= fb;
+                }
+            }
+            const float za = ma == -INFINITY ? 0.f : kWeightLog2 - ma, zb = mb == -INFINITY ? 0.f : kWeightLog2 - mb;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                pa[x] = exp2_fast(pa[x] + za);
+                pb[x] = exp2_fast(pb[x] + zb);
+                la += pa[x];
+                lb += pb[x];
+            }
+            const uint32_t a[4] = {pack_half2(pa[0], pa[1]), pack_half2(pb[0], pb[1]), pack_half2(pa[2], pa[3]),
+                                   pack_half2(pb[2], pb[3])};
+            // V of keys 2c, 2c + 1 and 8 + 2c, 9 + 2c, dims 16 j8 .. + 15
+            uint32_t vb[2][16];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int tok = t * 8 + 2 * c;
+                const uint2 u0 = *reinterpret_cast<const uint2*>(V + tok * 64 + j8 * 8);
+                const uint2 u1 = *reinterpret_cast<const uint2*>(V + tok * 64 + 64 + j8 * 8);
+                uint32_t b0 = V[kCodes + tok * 8 + j8], b1 = V[kCodes + tok * 8 + 8 + j8];
+                if (edge) {  // keys past the last row's: whatever their bytes say, they add nothing
+                    if (key0 + tok >= ke) b0 = 0;
+                    if (key0 + tok + 1 >= ke) b1 = 0;
+                }
+                const uint32_t s2 = e4m3x2_to_f16x2(b0 | b1 << 8);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    // bytes of (key, key + 1) codes: even dims, then odd dims
+                    const uint32_t w0 = x ? u0.y : u0.x, w1 = x ? u1.y : u1.x;
+                    const uint32_t ev = (w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u);
+                    const uint32_t od = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
+                    uint32_t f[4];
+                    e2m1x8_to_f16x2(ev, f);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) vb[t][8 * x + 2 * y] = hmul2(f[y], s2);
+                    e2m1x8_to_f16x2(od, f);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) vb[t][8 * x + 2 * y + 1] = hmul2(f[y], s2);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < 16; ++t) mma_f16(o[t], a, vb[0][t], vb[1][t]);
+        }
+        __syncwarp();  // every lane has read the stage
+        if (issued < mine) issue();
+    }
+    if (!ok) {  // copies still in flight land before the CTA's memory is given up
+        for (int s = 0; s < kStages; ++s)
+            if ((have >> s) & 1) mbar_wait_bounded(smem_u32(&bars[warp][s]), (phase >> s) & 1, nullptr, 200000000LL);
+    }
+    la += __shfl_xor_sync(0xffffffffu, la, 1);
+    la += __shfl_xor_sync(0xffffffffu, la, 2);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+    // join the warps: (m, l) and O through the rings' memory
+    if (c == 0) {
+        s_ml[warp][j8] = make_float2(ma, la);
+        s_ml[warp][j8 + 8] = make_float2(mb, lb);
+    }
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(&ring[0][0][0]);  // [kWarps][kRows][kPad]
+    constexpr int kPad = HD + 4;
+    static_assert(kWarps * kRows * kPad * 4 <= (int)sizeof(ring), "O of every warp fits in the rings");
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float* dst = so + (warp * kRows + j8 + 8 * half) * kPad;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int t = 0; t < 16; t += 4)
+                *reinterpret_cast<float4*>(dst + 16 * (2 * c + x) + t) =
+                    make_float4(o[t][2 * half + x], o[t + 1][2 * half + x], o[t + 2][2 * half + x], o[t + 3][2 * half + x]);
+    }
+    __syncthreads();
+    for (int r = warp; r < kRows && q0 + r < rows; r += kWarps) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][r].x);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = s_ml[w][r].x == -INFINITY ? 0.f : exp2_fast(s_ml[w][r].x - m);
+            l += f * s_ml[w][r].y;
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * kPad + 4 * lane);
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        const int qr = q0 + r;
+        const int64_t at = (row0 + qr / g) * p.hq + h * g + qr % g;
+        if (nsplit == 1) {
+            const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+            *reinterpret_cast<float4*>(p.part_o + (at * p.max_splits + sp) * HD + 4 * lane) = acc;
+            if (lane == 0) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
+        }
+    }
+}
+
+// The key chunks of every (row, query head) joined: one warp each, lane s
+// holding chunk s's (m, l).
+__global__ void __launch_bounds__(256) attn_kv4_merge_kernel(const AttnKv4Params p) {
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x & 31;
+    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (at >= (int64_t)p.n_seq * p.stride * p.hq) return;
+    const int64_t row = at / p.hq;
+    const int head = (int)(at - row * p.hq), b = (int)(row / p.stride), r = (int)(row - (int64_t)b * p.stride);
+    const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride), g = p.hq / p.hkv;
+    if (r >= n || S < 0 || (int64_t)S + n > p.max_ctx) return;
+    const int q0 = (r * g + head % g) / kRows * kRows;
+    const int nsplit = (tile_end(S, n * g, q0, g) + p.chunk - 1) / p.chunk;
+    if (nsplit <= 1) return;
+    const float2 ml = lane < nsplit ? __ldcg(p.part_ml + at * p.max_splits + lane) : make_float2(-INFINITY, 0.f);
+    const float m = warp_max(ml.x);
+    const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+    const float l = warp_sum(w * ml.y);
+    const float wl = l > 0.f || l != l ? w * p.v_scale / l : 0.f;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < nsplit; s0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            v[x] = s0 + x < nsplit ? __ldcg(po + (int64_t)(s0 + x) * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float f = __shfl_sync(0xffffffffu, wl, (s0 + x) & 31);
+            acc.x += f * v[x].x;
+            acc.y += f * v[x].y;
+            acc.z += f * v[x].z;
+            acc.w += f * v[x].w;
+        }
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// ---------------------------------------------------------------------------
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct AttnKv4Plan {
+    int chunk, max_splits, tiles;
+    size_t off_ml, off_o, bytes;
+};
+
+bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4Plan* w) {
+    if (n_seq < 1 || stride < 1 || stride > 1024 || hq < 1 || hkv < 1 || hq % hkv || hq / hkv > 128 || max_ctx < 1)
+        return false;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int g = hq / hkv;
+    w->tiles = (stride * g + kRows - 1) / kRows;
+    // Chunks by the call's capacity alone (a sequence's result does not depend on
+    // its neighbours' lengths): about one item per resident CTA when the
+    // sequences are at half the capacity, 256 to 2048 keys.
+    const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
+    const int64_t blocks = pairs * std::max(1, (max_ctx / 2 + 63) / 64);
+    int64_t cb = (blocks + 3LL * sms - 1) / (3LL * sms);
+    cb = std::max<int64_t>(4, std::min<int64_t>(cb, kMaxChunk / 64));
+    cb = std::max<int64_t>(cb, ((int64_t)max_ctx + 64LL * kMaxSplits - 1) / (64LL * kMaxSplits));
+    w->chunk = (int)std::min<int64_t>(cb * 64, 1 << 30);
+    w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
+    const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
+    w->off_ml = 256;
+    w->off_o = w->off_ml + round256(parts * sizeof(float2));
+    w->bytes = w->off_o + round256(parts * HD * sizeof(float));
+    return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
+}
+
+bool power_of_two(float x) {
+    int e;
+    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e > -60 && e < 60;
+}
+
+wedlm_status rows_params(RowsParams* p, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                         int64_t v_stride, void* pool, int32_t num_pages, int32_t hkv, const int32_t* table,
+                         int32_t pages_per_seq, const int32_t* S, const int32_t* n, int32_t n_seq, int32_t stride,
+                         float k_scale, float v_scale, void* err) {
+    if (n_seq < 0 || stride < 1 || hkv < 1 || num_pages < 1 || pages_per_seq < 1) return WEDLM_ERR_INVALID_ARG;
+    if (dtype != WEDLM_DTYPE_F32 && dtype != WEDLM_DTYPE_BF16) return WEDLM_ERR_UNSUPPORTED;
+    if (!power_of_two(k_scale) || !power_of_two(v_scale)) return WEDLM_ERR_INVALID_ARG;
+    const int vec = dtype == WEDLM_DTYPE_F32 ? 4 : 8;
+    if (k_stride < (int64_t)hkv * HD || v_stride < (int64_t)hkv * HD || k_stride % vec || v_stride % vec)
+        return WEDLM_ERR_INVALID_ARG;
+    if (n_seq > 0 && (!k || !v || !pool || !table || !S || !n || !err)) return WEDLM_ERR_INVALID_ARG;
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)pool) & 15) return WEDLM_ERR_INVALID_ARG;
+    if (((uintptr_t)table | (uintptr_t)S | (uintptr_t)n | (uintptr_t)err) & 3) return WEDLM_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)n_seq * stride;
+    if (rows > (int64_t)INT32_MAX * 256 / 16 / hkv) return WEDLM_ERR_INVALID_ARG;
+    *p = RowsParams{static_cast<uint8_t*>(pool), table, S, n, static_cast<int*>(err), rows * hkv * 16, k_stride,
+                    v_stride, num_pages, hkv, pages_per_seq, stride, k_scale, v_scale};
+    return WEDLM_OK;
+}
+
+}  // namespace
+}  // namespace wedlm
+
+using namespace wedlm;
+
+extern "C" {
+
+wedlm_status wedlm_kv4_append(const void* k, const void* v, int32_t dtype, int64_t k_stride, int64_t v_stride,
+                              void* kv4_pool, int32_t num_pages, int32_t n_kv_heads, const int32_t* page_table,
+                              int32_t pages_per_seq, const int32_t* S, const int32_t* n, int32_t n_seq,
+                              int32_t stride, float k_scale, float v_scale, void* error_word, void* stream) {
+    RowsParams p;
+    const wedlm_status s = rows_params(&p, k, v, dtype, k_stride, v_stride, kv4_pool, num_pages, n_kv_heads, page_table,
+                                       pages_per_seq, S, n, n_seq, stride, k_scale, v_scale, error_word);
+    if (s || p.total == 0) return s;
+    const dim3 grid((unsigned)((p.total + 255) / 256));
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e =
+        dtype == WEDLM_DTYPE_F32
+            ? launch_pdl(kv4_append_kernel<float>, grid, dim3(256), 0, st, (const float*)k, (const float*)v, p)
+            : launch_pdl(kv4_append_kernel<bf16>, grid, dim3(256), 0, st, (const bf16*)k, (const bf16*)v, p);
+    return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
+}
+
+wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_kv_heads, const int32_t* page_table,
+                            int32_t pages_per_seq, const int32_t* S, const int32_t* n, int32_t n_seq, int32_t stride,
+                            float k_scale, float v_scale, void* k, void* v, int32_t dtype, int64_t k_stride,
+                            int64_t v_stride, void* error_word, void* stream) {
+    RowsParams p;
+    const wedlm_status s = rows_params(&p, k, v, dtype, k_stride, v_stride, const_cast<void*>(kv4_pool), num_pages,
+                                       n_kv_heads, page_table, pages_per_seq, S, n, n_seq, stride, k_scale, v_scale,
+                                       error_word);
+    if (s || p.total == 0) return s;
+    const dim3 grid((unsigned)((p.total + 255) / 256));
+    cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e = dtype == WEDLM_DTYPE_F32
+                              ? launch_pdl(kv4_read_kernel<float>, grid, dim3(256), 0, st, (float*)k, (float*)v, p)
+                              : launch_pdl(kv4_read_kernel<bf16>, grid, dim3(256), 0, st, (bf16*)k, (bf16*)v, p);
+    return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
+}
+
+wedlm_status wedlm_attention_kv4_workspace_bytes(int32_t n_seq, int32_t stride, int32_t n_heads, int32_t n_kv_heads,
+                                                 int32_t max_ctx, int64_t* bytes) {
+    AttnKv4Plan w;
+    if (!bytes || !plan_attn_kv4(n_seq, stride, n_heads, n_kv_heads, max_ctx, &w)) return WEDLM_ERR_INVALID_ARG;
+    *bytes = (int64_t)w.bytes;
+    return WEDLM_OK;
+}
+
+wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t num_pages, int32_t n_heads,
+                                 int32_t n_kv_heads, const int32_t* page_table, int32_t pages_per_seq,
+                                 const int32_t* S, const int32_t* n, int32_t n_seq, int32_t stride, int32_t max_ctx,
+                                 float k_scale, float v_scale, void* out, void* workspace, int64_t workspace_bytes,
+                                 void* stream) {
+    AttnKv4Plan w;
+    if (!plan_attn_kv4(n_seq, stride, n_heads, n_kv_heads, max_ctx, &w)) return WEDLM_ERR_INVALID_ARG;
+    if (!q || !kv4_pool || !page_table || !S || !n || !out || !workspace || num_pages < 1 || pages_per_seq < 1)
+        return WEDLM_ERR_INVALID_ARG;
+    if (!power_of_two(k_scale) || !power_of_two(v_scale)) return WEDLM_ERR_INVALID_ARG;
+    if (workspace_bytes < (int64_t)w.bytes || ((uintptr_t)workspace & 255)) return WEDLM_ERR_INVALID_ARG;
+    if (((uintptr_t)q | (uintptr_t)kv4_pool | (uintptr_t)out) & 15) return WEDLM_ERR_INVALID_ARG;
+    if (((uintptr_t)page_table | (uintptr_t)S | (uintptr_t)n) & 3) return WEDLM_ERR_INVALID_ARG;
+    char* ws = static_cast<char*>(workspace);
+    cudaStream_t st = (cudaStream_t)stream;
+    const AttnKv4Params p{(const bf16*)q, (const uint8_t*)kv4_pool, page_table, S, n, (bf16*)out,
+                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (int*)ws, num_pages, n_heads, n_kv_heads,
+                          pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits, w.tiles, k_scale, v_scale};
+    const int64_t ctas = (int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits;
+    cudaError_t e = launch_pdl(attn_kv4_kernel, dim3((unsigned)ctas), dim3(kWarps * 32), 0, st, p);
+    if (e == cudaSuccess && w.max_splits > 1) {
+        const int64_t pairs = (int64_t)n_seq * stride * n_heads;
+        e = launch_pdl(attn_kv4_merge_kernel, dim3((unsigned)((pairs + 7) / 8)), dim3(256), 0, st, p);
+    }
+    return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
+}
+
+}  // extern "C"
