@@ -522,7 +522,8 @@ wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_k
  * appended; rows r >= n[b] are not written; stride <= 1024), with pointers
  * 16-byte aligned and the workspace 256-byte aligned, from
  * wedlm_attention_kv4_workspace_bytes.  The workspace's first int32 is the
- * device error word: zero it once, calls only ever set it (1: a page id outside
+ * device error word.  Zero the whole workspace once: calls leave its counters as
+ * they found them and only ever set the error word (1: a page id outside
  * [0, num_pages), whose 16 keys are then left out, or S[b] + n[b] > max_ctx or
  * S[b] < 0, whose rows are not written; 2: a bounded wait gave up).  The cache
  * enters the products unrounded; q and the softmax weights are rounded to 11

@@ -369,46 +369,48 @@ def attention_error(workspace) -> int:
 # not the documented one.  stream: a torch.cuda.Stream or a cudaStream_t handle;
 # None is torch's current stream of the tensors' device.  Results a call
 # allocates belong to that stream.
+# A decode step makes one such call per layer, so the checks are kept to a
+# microsecond or two.
 def _want(cond, what):
     if not cond:
         raise ValueError(what)
 
 
-def _on(t, device, dtype, shape, name):
-    """A contiguous tensor of the given device, dtype and shape."""
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: wants a contiguous {dtype} tensor of shape {shape} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+def _on(t, index, dtype, shape, name):
+    """A contiguous tensor of the given dtype and shape on CUDA device `index`."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: wants a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _cuda(t, name):
-    _want(t.is_cuda, f"{name}: wants a CUDA tensor")
-    return t.device
+def _index(t, name):
+    """The index of a tensor's CUDA device."""
+    index = t.get_device()
+    _want(index >= 0, f"{name}: wants a CUDA tensor")
+    return index
 
 
-class _Launch:
-    """The tensors' device made current and the stream to launch on, as a context."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.device = torch.cuda.device(device)
-        self.handle = torch.cuda.current_stream(device).cuda_stream if stream is None else _stream_handle(stream)
-
-    def __enter__(self):
-        self.device.__enter__()
-        return self.handle
-
-    def __exit__(self, *a):
-        self.device.__exit__(*a)
+def _launch(name, index, stream, *args):
+    """Call the library with device `index` current, the stream as last argument."""
+    import torch
+    fn = getattr(_lib.load(), name)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
+    if st != 0:
+        _check(st, name)
 
 
-def _empty_on(stream, device, shape, dtype):
+def _empty_on(stream, index, shape, dtype):
     """A new tensor of the launch's stream (of the current one for a plain handle)."""
     import torch
     if stream is None or isinstance(stream, int):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=index)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
 def kv4_pool(num_pages: int, n_kv_heads: int, n_layers: int | None = None, device="cuda"):
@@ -418,26 +420,27 @@ def kv4_pool(num_pages: int, n_kv_heads: int, n_layers: int | None = None, devic
     return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
 
 
-def _kv4_args(kv4_pool, page_table, S, n, device):
+def _kv4_args(kv4_pool, page_table, S, n, index):
     import torch
     half = C["WEDLM_KV4_HALF_PAGE"]
-    _want(kv4_pool.dim() == 4 and kv4_pool.shape[2:] == (2, half), f"kv4_pool: wants [pages, kv heads, 2, {half}]")
-    _on(kv4_pool, device, torch.uint8, tuple(kv4_pool.shape), "kv4_pool")
+    pool, n_seq = kv4_pool.shape, page_table.shape[0]
+    _want(len(pool) == 4 and pool[2] == 2 and pool[3] == half, f"kv4_pool: wants [pages, kv heads, 2, {half}]")
     _want(page_table.dim() == 2, "page_table: wants [n_seq, pages_per_seq]")
-    n_seq = page_table.shape[0]
-    _on(page_table, device, torch.int32, tuple(page_table.shape), "page_table")
-    _on(S, device, torch.int32, (n_seq,), "S")
-    _on(n, device, torch.int32, (n_seq,), "n")
-    return n_seq, kv4_pool.shape[0], kv4_pool.shape[1]
+    _on(kv4_pool, index, torch.uint8, pool, "kv4_pool")
+    _on(page_table, index, torch.int32, page_table.shape, "page_table")
+    _on(S, index, torch.int32, (n_seq,), "S")
+    _on(n, index, torch.int32, (n_seq,), "n")
+    return n_seq, pool[0], pool[1]
 
 
-def _rows_arg(t, rows, hkv, device, dtype, name):
+def _rows_arg(t, rows, hkv, index, dtype, name):
     """Rows [rows, hkv, 128] whose heads lie side by side; any row stride the library takes."""
-    if (t.dim() != 3 or tuple(t.shape) != (rows, hkv, 128) or t.device != device or t.dtype != dtype
-            or t.stride(2) != 1 or (hkv > 1 and t.stride(1) != 128)):
-        raise ValueError(f"{name}: wants {dtype} [{rows}, {hkv}, 128] on {device} with the heads of a row side by "
-                         f"side, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t.stride(0) if rows > 1 else hkv * 128
+    st = t.stride()
+    if (t.shape != (rows, hkv, 128) or t.get_device() != index or t.dtype != dtype or st[2] != 1
+            or (hkv > 1 and st[1] != 128)):
+        raise ValueError(f"{name}: wants {dtype} [{rows}, {hkv}, 128] on cuda:{index} with the heads of a row side by "
+                         f"side, got {t.dtype} {tuple(t.shape)} strides {st} on {t.device}")
+    return st[0] if rows > 1 else hkv * 128
 
 
 def _rows_dtype(dtype):
@@ -448,9 +451,9 @@ def _rows_dtype(dtype):
     return C["WEDLM_DTYPE_BF16"]
 
 
-def _error_word(t, device):
+def _error_word(t, index):
     import torch
-    _want(t.device == device and t.is_contiguous() and t.dtype in (torch.int32, torch.uint8) and
+    _want(t.get_device() == index and t.is_contiguous() and t.dtype in (torch.int32, torch.uint8) and
           t.numel() * t.element_size() >= 4, "error: wants an int32 tensor or a workspace on the same device")
 
 
@@ -461,16 +464,15 @@ def kv4_append(k, v, kv4_pool, page_table, S, n, stride: int, error, k_scale: fl
     are taken as they are); kv4_pool from kv4_pool(); page_table [n_seq,
     pages_per_seq], S, n [n_seq] int32; error: an int32 tensor, or the workspace
     of attention_kv4, whose first word records errors (attention_error)."""
-    device = _cuda(k, "k")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
-    ks = _rows_arg(k, n_seq * stride, hkv, device, k.dtype, "k")
-    vs = _rows_arg(v, n_seq * stride, hkv, device, k.dtype, "v")
-    _error_word(error, device)
-    dt = _rows_dtype(k.dtype)
-    with _Launch(device, stream) as st:
-        _check(_lib.load().wedlm_kv4_append(_ptr(k), _ptr(v), dt, ks, vs, _ptr(kv4_pool), pages, hkv, _ptr(page_table),
-                                            page_table.shape[1], _ptr(S), _ptr(n), n_seq, stride, k_scale, v_scale,
-                                            _ptr(error), st), "wedlm_kv4_append")
+    index = _index(k, "k")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
+    dtype = k.dtype
+    ks = _rows_arg(k, n_seq * stride, hkv, index, dtype, "k")
+    vs = _rows_arg(v, n_seq * stride, hkv, index, dtype, "v")
+    _error_word(error, index)
+    _launch("wedlm_kv4_append", index, stream, k.data_ptr(), v.data_ptr(), _rows_dtype(dtype), ks, vs,
+            kv4_pool.data_ptr(), pages, hkv, page_table.data_ptr(), page_table.shape[1], S.data_ptr(), n.data_ptr(),
+            n_seq, stride, k_scale, v_scale, error.data_ptr())
 
 
 def kv4_read(kv4_pool, page_table, S, n, stride: int, error, dtype=None, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -478,22 +480,20 @@ def kv4_read(kv4_pool, page_table, S, n, stride: int, error, dtype=None, k_scale
     """Rows of a 4-bit cache, widened (wedlm_kv4_read): (k, v), each
     [n_seq*stride, n_kv_heads, 128] in dtype (bfloat16 unless given), or written
     into out = (k, v).  Rows r >= n[b] are left as they are."""
-    import torch
-    device = _cuda(kv4_pool, "kv4_pool")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
+    index = _index(kv4_pool, "kv4_pool")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
     if out is None:
-        shape = (n_seq * stride, hkv, 128)
-        out = tuple(_empty_on(stream, device, shape, dtype or torch.bfloat16) for _ in range(2))
+        import torch
+        out = tuple(_empty_on(stream, index, (n_seq * stride, hkv, 128), dtype or torch.bfloat16) for _ in range(2))
     k, v = out
     _want(dtype is None or k.dtype == dtype, "out and dtype disagree")
-    ks = _rows_arg(k, n_seq * stride, hkv, device, k.dtype, "k")
-    vs = _rows_arg(v, n_seq * stride, hkv, device, k.dtype, "v")
-    _error_word(error, device)
-    dt = _rows_dtype(k.dtype)
-    with _Launch(device, stream) as st:
-        _check(_lib.load().wedlm_kv4_read(_ptr(kv4_pool), pages, hkv, _ptr(page_table), page_table.shape[1], _ptr(S),
-                                          _ptr(n), n_seq, stride, k_scale, v_scale, _ptr(k), _ptr(v), dt, ks, vs,
-                                          _ptr(error), st), "wedlm_kv4_read")
+    dtype = k.dtype
+    ks = _rows_arg(k, n_seq * stride, hkv, index, dtype, "k")
+    vs = _rows_arg(v, n_seq * stride, hkv, index, dtype, "v")
+    _error_word(error, index)
+    _launch("wedlm_kv4_read", index, stream, kv4_pool.data_ptr(), pages, hkv, page_table.data_ptr(),
+            page_table.shape[1], S.data_ptr(), n.data_ptr(), n_seq, stride, k_scale, v_scale, k.data_ptr(),
+            v.data_ptr(), _rows_dtype(dtype), ks, vs, error.data_ptr())
     return k, v
 
 
@@ -514,21 +514,19 @@ def attention_kv4(q, kv4_pool, page_table, S, n, stride: int, n_heads: int, n_kv
     workspace from attention_kv4_workspace() with the same sizes.  Returns `out`;
     read attention_error(workspace) after synchronising."""
     import torch
-    device = _cuda(q, "q")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, device)
+    index = _index(q, "q")
+    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
     _want(hkv == n_kv_heads, "kv4_pool has another number of KV heads")
     shape = (n_seq * stride, n_heads, 128)
-    _on(q, device, torch.bfloat16, shape, "q")
+    _on(q, index, torch.bfloat16, shape, "q")
     if out is None:
-        out = _empty_on(stream, device, shape, torch.bfloat16)
+        out = _empty_on(stream, index, shape, torch.bfloat16)
     else:
-        _on(out, device, torch.bfloat16, shape, "out")
-    _on(workspace, device, torch.uint8, tuple(workspace.shape), "workspace")
-    with _Launch(device, stream) as st:
-        _check(_lib.load().wedlm_attention_kv4(_ptr(q), _ptr(kv4_pool), pages, n_heads, hkv, _ptr(page_table),
-                                               page_table.shape[1], _ptr(S), _ptr(n), n_seq, stride, max_ctx, k_scale,
-                                               v_scale, _ptr(out), _ptr(workspace), workspace.numel(), st),
-               "wedlm_attention_kv4")
+        _on(out, index, torch.bfloat16, shape, "out")
+    _on(workspace, index, torch.uint8, workspace.shape, "workspace")
+    _launch("wedlm_attention_kv4", index, stream, q.data_ptr(), kv4_pool.data_ptr(), pages, n_heads, hkv,
+            page_table.data_ptr(), page_table.shape[1], S.data_ptr(), n.data_ptr(), n_seq, stride, max_ctx, k_scale,
+            v_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -544,57 +542,59 @@ class KVPages:
 
     def __init__(self, pool, page_table, S, refs, workspace=None):
         import torch
-        self.device = device = _cuda(pool, "pool")
-        _want(pool.dim() >= 3 and pool[0].is_contiguous(), "pool: wants [n_layers, num_pages, ...] with contiguous layers")
+        self.index = index = _index(pool, "pool")
+        _want(pool.dim() >= 3 and pool.numel() > 0 and pool[0].is_contiguous(),
+              "pool: wants [n_layers, num_pages, ...] with contiguous layers")
         layers, pages = pool.shape[:2]
         _want(page_table.dim() == 2, "page_table: wants [n_seq, pages_per_seq]")
         n_seq = page_table.shape[0]
-        _on(page_table, device, torch.int32, tuple(page_table.shape), "page_table")
-        _on(S, device, torch.int32, (n_seq,), "S")
-        _on(refs, device, torch.int32, (pages,), "refs")
+        _on(page_table, index, torch.int32, page_table.shape, "page_table")
+        _on(S, index, torch.int32, (n_seq,), "S")
+        _on(refs, index, torch.int32, (pages,), "refs")
         nb = ctypes.c_int64()
         _check(_lib.load().wedlm_kv_pages_workspace_bytes(pages, n_seq, ctypes.byref(nb)),
                "wedlm_kv_pages_workspace_bytes")
         if workspace is None:
-            workspace = torch.zeros(int(nb.value), dtype=torch.uint8, device=device)
-        _on(workspace, device, torch.uint8, tuple(workspace.shape), "workspace")
+            workspace = torch.zeros(int(nb.value), dtype=torch.uint8, device=index)
+        _on(workspace, index, torch.uint8, workspace.shape, "workspace")
         self.pool, self.page_table, self.S, self.refs, self.workspace = pool, page_table, S, refs, workspace
         size = pool.element_size()
         stride = pool.stride(0) if layers > 1 else pool[0].numel()
         self._desc = _lib.KVPagesDesc(_ptr(pool), stride * size, pool[0, 0].numel() * size, _ptr(page_table), _ptr(S),
                                       _ptr(refs), layers, pages, n_seq, page_table.shape[1])
         self._by = ctypes.byref(self._desc)
+        self._ws = (workspace.data_ptr(), workspace.numel())
 
     def _list(self, t, name, n=None):
         import torch
-        _on(t, self.device, torch.int32, (t.numel() if n is None else n,), name)
+        _on(t, self.index, torch.int32, (t.numel() if n is None else n,), name)
         return t.numel()
 
     def _call(self, name, stream, *args):
-        with _Launch(self.device, stream) as st:
-            _check(getattr(_lib.load(), name)(self._by, *args, _ptr(self.workspace), self.workspace.numel(), st), name)
+        _launch(name, self.index, stream, self._by, *args, *self._ws)
 
     def copy(self, src, dst, stream=None):
         """Page dst[i] := page src[i] in every layer."""
         n = self._list(src, "src")
         self._list(dst, "dst", n)
-        self._call("wedlm_kv_pages_copy", stream, _ptr(src), _ptr(dst), n)
+        self._call("wedlm_kv_pages_copy", stream, src.data_ptr(), dst.data_ptr(), n)
 
     def reserve(self, seqs, tokens, stream=None):
         """Free pages for seqs[i] until it has room for tokens[i] tokens."""
         n = self._list(seqs, "seqs")
         self._list(tokens, "tokens", n)
-        self._call("wedlm_kv_pages_reserve", stream, _ptr(seqs), _ptr(tokens), n)
+        self._call("wedlm_kv_pages_reserve", stream, seqs.data_ptr(), tokens.data_ptr(), n)
 
     def fork(self, parents, children, stream=None):
         """children[i], an empty sequence, becomes a copy of parents[i] that shares its full pages."""
         n = self._list(parents, "parents")
         self._list(children, "children", n)
-        self._call("wedlm_kv_pages_fork", stream, _ptr(parents), _ptr(children), n)
+        self._call("wedlm_kv_pages_fork", stream, parents.data_ptr(), children.data_ptr(), n)
 
     def free(self, seqs, stream=None):
         """Drop the sequences: their pages lose a reference, rows become -1 and S 0."""
-        self._call("wedlm_kv_pages_free", stream, _ptr(seqs), self._list(seqs, "seqs"))
+        n = self._list(seqs, "seqs")
+        self._call("wedlm_kv_pages_free", stream, seqs.data_ptr(), n)
 
     def compact(self, map=None, stream=None):
         """Move the u pages in use to ids 0 .. u - 1; map [num_pages] int32 receives the new ids."""

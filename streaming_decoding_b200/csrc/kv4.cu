@@ -222,15 +222,17 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // Attention over the 4-bit cache: out = softmax(q K^T / sqrt(128)) V of window
 // rows r over cache positions 0 .. S + r, as wedlm_attention_bf16.
 //
-// Work item (a CTA of four warps): 16 query rows (window rows x the g heads
-// that share a KV head), one KV head, one chunk of keys; the warps take the
-// chunk's pages in turn, each with its own ring of page buffers filled by bulk
-// copies, and join their results at the end.  Codes go from shared memory to
-// registers, are widened and scaled there and feed mma.sync directly: no
-// widened copy of K or V is ever written anywhere.  For this the dims are
-// permuted inside the products (which changes no sum): in q K^T the lanes of a
-// quad own 32 consecutive dims each, so a lane's operands of a key are 16
-// consecutive bytes; in P V a lane owns the 16 dims of one scale block.
+// Work item (a CTA of four warps): NT * 8 query rows (window rows x the g
+// heads that share a KV head), one KV head, one chunk of keys; the warps take
+// the chunk's pages in turn, each with its own ring of page buffers filled by
+// bulk copies, and join their results at the end.  Codes go from shared memory
+// to registers, are widened and scaled there and feed mma.sync directly: no
+// widened copy of K or V is ever written anywhere.  The cache is the M side of
+// both products (S^T = K Q^T, O^T = V^T P^T), so that a token's 4 to 8 query
+// rows fill the 8-wide N side; P^T is S^T transposed in registers.  The dims
+// are permuted inside the products (which changes no sum): in K Q^T the lanes
+// of a quad own 32 consecutive dims each, so a lane's operands of a key are 16
+// consecutive bytes; in V^T P^T a lane owns the 16 dims of one scale block.
 //
 // Q is held in fp16 scaled per row by a power of two (its largest element in
 // [2^14, 2^15)), which keeps every bit of a bf16 q that is within 2^-28 of the
@@ -240,7 +242,6 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // outputs are fp32.
 constexpr int kWarps = 4;
 constexpr int kStages = 4;
-constexpr int kRows = 16;
 constexpr int kMaxSplits = 32;
 constexpr int kMaxChunk = 2048;       // keys of a chunk, unless the context needs more per chunk
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum tolerated before O is rescaled
@@ -253,8 +254,9 @@ struct AttnKv4Params {
     const int32_t* S;
     const int32_t* n;
     bf16* out;
-    float* part_o;    // [rows][hq][max_splits][128]
-    float2* part_ml;  // [rows][hq][max_splits]
+    float* part_o;       // [rows][hq][max_splits][128]
+    float2* part_ml;     // [rows][hq][max_splits]
+    unsigned* tickets;   // [n_seq][hkv][tiles], zero between calls
     int* err;
     int num_pages, hq, hkv, pages_per_seq, n_seq, stride, max_ctx, chunk, max_splits, tiles;
     float k_scale, v_scale;
@@ -266,11 +268,19 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values (lane 4 i + c holds row i, columns 2c, 2c + 1) transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 
 __device__ __forceinline__ void bar_init(uint64_t* bar) {
@@ -284,11 +294,8 @@ __device__ __forceinline__ void load_page(void* dst, const uint8_t* src, uint64_
                  ::"r"(smem_u32(dst)), "l"(src), "r"(kHeadPage), "r"(smem_u32(bar)) : "memory");
 }
 
-// Key chunks of the 16-row tile that starts at query row q0.
-__device__ __forceinline__ int tile_end(int S, int rows, int q0, int g) { return S + (min(q0 + kRows, rows) - 1) / g + 1; }
-
-// A thread's 32 dims of one query row (32 c .. 32 c + 31), scaled to fp16: the
-// A operands of the 8 k-steps (two registers per step); returns the exponent
+// A lane's 32 dims of one query row (32 c .. 32 c + 31), scaled to fp16: the
+// operands of the 8 k-steps (two registers per step); returns the exponent
 // that was added.
 __device__ __forceinline__ int load_q(const bf16* q, bool live, uint32_t (&a)[16]) {
     uint32_t w[16];
@@ -313,10 +320,47 @@ __device__ __forceinline__ int load_q(const bf16* q, bool live, uint32_t (&a)[16
     return e;
 }
 
-__global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4Params p) {
+// The 16 rows of chunk results of one (row, head) joined and written; lane s
+// holds chunk s's (m, l), a lane writes four dims.
+__device__ __forceinline__ void join_splits(const AttnKv4Params& p, int64_t at, int nsplit, int lane) {
+    const float2 ml = lane < nsplit ? __ldcg(p.part_ml + at * p.max_splits + lane) : make_float2(-INFINITY, 0.f);
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + lane;
+    float4 v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        v[x] = x < nsplit ? __ldcg(po + (int64_t)x * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float m = warp_max(ml.x);
+    const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
+    const float l = warp_sum(w * ml.y);
+    const float wl = l > 0.f || l != l ? w * p.v_scale / l : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < nsplit; s0 += 8) {
+        if (s0 > 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                v[x] = s0 + x < nsplit ? __ldcg(po + (int64_t)(s0 + x) * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float f = __shfl_sync(0xffffffffu, wl, (s0 + x) & 31);
+            acc.x += f * v[x].x;
+            acc.y += f * v[x].y;
+            acc.z += f * v[x].z;
+            acc.w += f * v[x].w;
+        }
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 3) attn_kv4_kernel(const AttnKv4Params p) {
+    constexpr int kRows = 8 * NT;
     __shared__ __align__(128) uint8_t ring[kWarps][kStages][kHeadPage];
     __shared__ __align__(8) uint64_t bars[kWarps][kStages];
     __shared__ float2 s_ml[kWarps][kRows];
+    __shared__ int s_last;
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, j8 = lane >> 2;
@@ -328,69 +372,78 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4P
     id /= p.max_splits;
     const int h = (int)(id % p.hkv), b = (int)(id / p.hkv);
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
+    const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
+    const int ks = sp * p.chunk, page0 = ks / kPage;
+    // Page ids of this warp's pages, 32 at a time, one per lane; the first ones
+    // are read together with S and n.
+    auto raw_id = [&](int k) {
+        const int idx = page0 + warp + k * kWarps;
+        return idx < p.pages_per_seq && k * kWarps * kPage < p.chunk ? __ldcg(table + idx) : -1;
+    };
+    int ids = raw_id(lane);
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) bar_init(&bars[warp][s]);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
     const int rows = n * g, q0 = tile * kRows;
     if (n <= 0 || q0 >= rows) return;
     if (S < 0 || (int64_t)S + n > p.max_ctx) {
         if (threadIdx.x == 0) set_error(p.err, kErrBounds);
         return;
     }
-    const int kend = tile_end(S, rows, q0, g);
+    const int kend = S + (min(q0 + kRows, rows) - 1) / g + 1;
     const int nsplit = (kend + p.chunk - 1) / p.chunk;
     if (sp >= nsplit) return;
-    const int ks = sp * p.chunk, ke = min(kend, ks + p.chunk);
-    const int page0 = ks / kPage, npages = (ke + kPage - 1) / kPage - page0;
+    const int ke = min(kend, ks + p.chunk);
+    const int npages = (ke + kPage - 1) / kPage - page0;
     const int mine = npages > warp ? (npages - warp + kWarps - 1) / kWarps : 0;  // pages of this warp
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) bar_init(&bars[warp][s]);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    __syncwarp();
-    const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
-    // Page ids of this warp's pages, 32 at a time, one per lane (-1: none).
-    int ids = -1;
-    auto fetch_ids = [&](int first) {
-        const int k = first + lane;
-        ids = -1;
-        if (k < mine) {
-            const int idx = page0 + warp + k * kWarps;
-            ids = idx < p.pages_per_seq ? __ldcg(table + idx) : -1;
-            if (ids < 0 || ids >= p.num_pages) {
-                set_error(p.err, kErrBounds);
-                ids = -1;
-            }
-        }
-    };
     // Load k of this warp into its stage; a page outside the pool is not loaded
     // and its keys count as masked.
     uint32_t have = 0;  // bit s: the page in stage s was loaded
     int issued = 0;
     auto issue = [&]() {
-        if ((issued & 31) == 0) fetch_ids(issued);
+        if ((issued & 31) == 0 && issued > 0) ids = raw_id(issued + lane);
         const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
         const int s = issued % kStages;
         have &= ~(1u << s);
-        if (page >= 0) {
+        if (page >= 0 && page < p.num_pages) {
             have |= 1u << s;
             if (lane == 0)
                 load_page(ring[warp][s], p.pool + ((int64_t)page * p.hkv + h) * kHeadPage, &bars[warp][s]);
+        } else {
+            set_error(p.err, kErrBounds);
         }
         ++issued;
     };
     while (issued < min(mine, kStages)) issue();
 
-    // Q of rows j8 and j8 + 8 of the tile
-    uint32_t qa[16], qb[16];
-    const int ra = q0 + j8, rb = ra + 8;
+    // Q of row j8 of every n-tile (operand B) and, for the lane's own columns
+    // (queries 2c and 2c + 1 of every n-tile), score factors and last keys
+    uint32_t qf[NT][16];
+    float sl[NT][2];
+    int lim[NT][2], lim_min = ke - 1;
     const int64_t row0 = (int64_t)b * p.stride;
-    auto q_at = [&](int r) { return p.q + ((row0 + r / g) * p.hq + h * g + r % g) * HD + 32 * c; };
-    const int ea = load_q(q_at(min(ra, rows - 1)), ra < rows, qa);
-    const int eb = load_q(q_at(min(rb, rows - 1)), rb < rows, qb);
     const float base = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale;
-    const float sla = base * __int_as_float((127 - ea) << 23), slb = base * __int_as_float((127 - eb) << 23);
-    const int lima = min(S + min(ra, rows - 1) / g, ke - 1), limb = min(S + min(rb, rows - 1) / g, ke - 1);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = q0 + 8 * t + j8, rc = min(r, rows - 1);
+        const int e = load_q(p.q + ((row0 + rc / g) * p.hq + h * g + rc % g) * HD + 32 * c, r < rows, qf[t]);
+        const float f = base * __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            sl[t][x] = __shfl_sync(0xffffffffu, f, (2 * c + x) * 4);
+            lim[t][x] = min(S + min(q0 + 8 * t + 2 * c + x, rows - 1) / g, ke - 1);
+            lim_min = min(lim_min, lim[t][x]);
+        }
+    }
+    lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 1));
+    lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
 
-    float o[16][4] = {};
-    float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;  // maxima in the exp2 domain
+    float o[8][NT][4] = {};
+    float m[NT][2], l[NT][2] = {};  // maxima in the exp2 domain
+#pragma unroll
+    for (int t = 0; t < NT; ++t) m[t][0] = m[t][1] = -INFINITY;
     uint32_t phase = 0;
     bool ok = true;
     for (int k = 0; k < mine; ++k) {
@@ -403,80 +456,34 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4P
             const uint8_t* K = ring[warp][s];
             const uint8_t* V = K + kHalfPage;
             const int key0 = (page0 + warp + k * kWarps) * kPage;
-            // scores of the page's 16 keys (two n-tiles of 8)
-            float sc[2][4] = {};
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int tok = t * 8 + j8;
-                const uint4 u = *reinterpret_cast<const uint4*>(K + tok * 64 + c * 16);
-                const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + tok * 8 + c * 2));
-                const uint32_t slo = __byte_perm(s2, s2, 0x1010), shi = __byte_perm(s2, s2, 0x3232);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            const bool edge = key0 + kPage - 1 > lim_min;
+            // S^T of the page's 16 keys: lane's rows are keys j8 and j8 + 8
+            float sc[NT][4] = {};
+            {
+                const uint4 u0 = *reinterpret_cast<const uint4*>(K + j8 * 64 + c * 16);
+                const uint4 u1 = *reinterpret_cast<const uint4*>(K + (j8 + 8) * 64 + c * 16);
+                const uint32_t s0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + c * 2));
+                const uint32_t s1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + 64 + c * 2));
+                const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+                const uint32_t f0[2] = {__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)};
+                const uint32_t f1[2] = {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)};
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    uint32_t f[4];
-                    e2m1x8_to_f16x2(w[x], f);
-                    const uint32_t sx = x < 2 ? slo : shi;
+                    uint32_t a[4], d[4];
+                    e2m1x8_to_f16x2(w0[x], a);
+                    e2m1x8_to_f16x2(w1[x], d);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int st = 2 * x + y;
-                        const uint32_t a[4] = {qa[2 * st], qb[2 * st], qa[2 * st + 1], qb[2 * st + 1]};
-                        mma_f16(sc[t], a, hmul2(f[2 * y], sx), hmul2(f[2 * y + 1], sx));
+                        const uint32_t a0 = hmul2(a[2 * y], f0[x >> 1]), a1 = hmul2(d[2 * y], f1[x >> 1]);
+                        const uint32_t a2 = hmul2(a[2 * y + 1], f0[x >> 1]), a3 = hmul2(d[2 * y + 1], f1[x >> 1]);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            mma_f16(sc[t], a0, a1, a2, a3, qf[t][4 * x + 2 * y], qf[t][4 * x + 2 * y + 1]);
                     }
                 }
             }
-            const int lim_min = min(lima, limb);
-            const bool edge = __any_sync(0xffffffffu, key0 + kPage - 1 > lim_min);
-            float pa[4], pb[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    pa[2 * t + x] = sc[t][x] * sla;
-                    pb[2 * t + x] = sc[t][2 + x] * slb;
-                }
-            if (edge) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int key = key0 + t * 8 + 2 * c + x;
-                        if (key > lima) pa[2 * t + x] = -INFINITY;
-                        if (key > limb) pb[2 * t + x] = -INFINITY;
-                    }
-            }
-            float na = fmaxf(fmaxf(pa[0], pa[1]), fmaxf(pa[2], pa[3]));
-            float nb = fmaxf(fmaxf(pb[0], pb[1]), fmaxf(pb[2], pb[3]));
-            if (__any_sync(0xffffffffu, na > ma + kLazyLog2 || nb > mb + kLazyLog2)) {
-                na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, 1));
-                na = fmaxf(na, __shfl_xor_sync(0xffffffffu, na, 2));
-                nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 1));
-                nb = fmaxf(nb, __shfl_xor_sync(0xffffffffu, nb, 2));
-                const float fa = na > ma ? exp2_fast(ma - na) : 1.f, fb = nb > mb ? exp2_fast(mb - nb) : 1.f;
-                ma = fmaxf(ma, na);
-                mb = fmaxf(mb, nb);
-                la *= fa;
-                lb *= fb;
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    o[t][0] *= fa;
-                    o[t][1] *= fa;
-                    o[t][2] *= fb;
-                    o[t][3] *= fb;
-                }
-            }
-            const float za = ma == -INFINITY ? 0.f : kWeightLog2 - ma, zb = mb == -INFINITY ? 0.f : kWeightLog2 - mb;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                pa[x] = exp2_fast(pa[x] + za);
-                pb[x] = exp2_fast(pb[x] + zb);
-                la += pa[x];
-                lb += pb[x];
-            }
-            const uint32_t a[4] = {pack_half2(pa[0], pa[1]), pack_half2(pb[0], pb[1]), pack_half2(pa[2], pa[3]),
-                                   pack_half2(pb[2], pb[3])};
-            // V of keys 2c, 2c + 1 and 8 + 2c, 9 + 2c, dims 16 j8 .. + 15
-            uint32_t vb[2][16];
+            // V^T: lane's rows are dims 16 j8 .. + 15, its columns keys 2c, 2c + 1, 8 + 2c, 9 + 2c
+            uint32_t vf[2][16];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int tok = t * 8 + 2 * c;
@@ -497,14 +504,54 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4P
                     uint32_t f[4];
                     e2m1x8_to_f16x2(ev, f);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) vb[t][8 * x + 2 * y] = hmul2(f[y], s2);
+                    for (int y = 0; y < 4; ++y) vf[t][8 * x + 2 * y] = hmul2(f[y], s2);
                     e2m1x8_to_f16x2(od, f);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) vb[t][8 * x + 2 * y + 1] = hmul2(f[y], s2);
+                    for (int y = 0; y < 4; ++y) vf[t][8 * x + 2 * y + 1] = hmul2(f[y], s2);
                 }
             }
+            bool grew = false;
 #pragma unroll
-            for (int t = 0; t < 16; ++t) mma_f16(o[t], a, vb[0][t], vb[1][t]);
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    sc[t][x] *= sl[t][x & 1];
+                    if (edge && key0 + j8 + 8 * (x >> 1) > lim[t][x & 1]) sc[t][x] = -INFINITY;
+                }
+                grew |= fmaxf(sc[t][0], sc[t][2]) > m[t][0] + kLazyLog2 || fmaxf(sc[t][1], sc[t][3]) > m[t][1] + kLazyLog2;
+            }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v = fmaxf(sc[t][x], sc[t][2 + x]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                        const float f = v > m[t][x] ? exp2_fast(m[t][x] - v) : 1.f;
+                        m[t][x] = fmaxf(m[t][x], v);
+                        l[t][x] *= f;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            o[u][t][x] *= f;
+                            o[u][t][2 + x] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float z = m[t][x & 1] == -INFINITY ? 0.f : kWeightLog2 - m[t][x & 1];
+                    sc[t][x] = exp2_fast(sc[t][x] + z);
+                    l[t][x & 1] += sc[t][x];
+                }
+                const uint32_t b0 = transpose8x8(pack_half2(sc[t][0], sc[t][1]));
+                const uint32_t b1 = transpose8x8(pack_half2(sc[t][2], sc[t][3]));
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    mma_f16(o[u][t], vf[0][2 * u], vf[0][2 * u + 1], vf[1][2 * u], vf[1][2 * u + 1], b0, b1);
+            }
         }
         __syncwarp();  // every lane has read the stage
         if (issued < mine) issue();
@@ -513,40 +560,40 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4P
         for (int s = 0; s < kStages; ++s)
             if ((have >> s) & 1) mbar_wait_bounded(smem_u32(&bars[warp][s]), (phase >> s) & 1, nullptr, 200000000LL);
     }
-    la += __shfl_xor_sync(0xffffffffu, la, 1);
-    la += __shfl_xor_sync(0xffffffffu, la, 2);
-    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-    // join the warps: (m, l) and O through the rings' memory
-    if (c == 0) {
-        s_ml[warp][j8] = make_float2(ma, la);
-        s_ml[warp][j8 + 8] = make_float2(mb, lb);
-    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], d);
+            if (j8 == 0) s_ml[warp][8 * t + 2 * c + x] = make_float2(m[t][x], l[t][x]);
+        }
+    // join the warps: O through the rings' memory
     __syncthreads();
-    float* so = reinterpret_cast<float*>(&ring[0][0][0]);  // [kWarps][kRows][kPad]
     constexpr int kPad = HD + 4;
+    float* so = reinterpret_cast<float*>(&ring[0][0][0]);  // [kWarps][kRows][kPad]
     static_assert(kWarps * kRows * kPad * 4 <= (int)sizeof(ring), "O of every warp fits in the rings");
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float* dst = so + (warp * kRows + j8 + 8 * half) * kPad;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < 2; ++x) {
+            float* dst = so + (warp * kRows + 8 * t + 2 * c + x) * kPad + 16 * j8;
 #pragma unroll
-            for (int t = 0; t < 16; t += 4)
-                *reinterpret_cast<float4*>(dst + 16 * (2 * c + x) + t) =
-                    make_float4(o[t][2 * half + x], o[t + 1][2 * half + x], o[t + 2][2 * half + x], o[t + 3][2 * half + x]);
-    }
+            for (int u = 0; u < 8; u += 2)
+                *reinterpret_cast<float4*>(dst + 2 * u) =
+                    make_float4(o[u][t][x], o[u][t][2 + x], o[u + 1][t][x], o[u + 1][t][2 + x]);
+        }
     __syncthreads();
     for (int r = warp; r < kRows && q0 + r < rows; r += kWarps) {
-        float m = -INFINITY;
+        float mm = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][r].x);
-        float l = 0.f;
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r].x);
+        float ll = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = s_ml[w][r].x == -INFINITY ? 0.f : exp2_fast(s_ml[w][r].x - m);
-            l += f * s_ml[w][r].y;
+            const float f = s_ml[w][r].x == -INFINITY ? 0.f : exp2_fast(s_ml[w][r].x - mm);
+            ll += f * s_ml[w][r].y;
             const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * kPad + 4 * lane);
             acc.x += f * v.x;
             acc.y += f * v.y;
@@ -556,65 +603,38 @@ __global__ void __launch_bounds__(kWarps * 32, 3) attn_kv4_kernel(const AttnKv4P
         const int qr = q0 + r;
         const int64_t at = (row0 + qr / g) * p.hq + h * g + qr % g;
         if (nsplit == 1) {
-            const float inv = l > 0.f || l != l ? p.v_scale / l : 0.f;
+            const float inv = ll > 0.f || ll != ll ? p.v_scale / ll : 0.f;
             const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
             *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
                 make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
         } else {
             *reinterpret_cast<float4*>(p.part_o + (at * p.max_splits + sp) * HD + 4 * lane) = acc;
-            if (lane == 0) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
+            if (lane == 0) p.part_ml[at * p.max_splits + sp] = make_float2(mm, ll);
         }
     }
-}
-
-// The key chunks of every (row, query head) joined: one warp each, lane s
-// holding chunk s's (m, l).
-__global__ void __launch_bounds__(256) attn_kv4_merge_kernel(const AttnKv4Params p) {
-    griddep_wait();
-    griddep_launch();
-    const int lane = threadIdx.x & 31;
-    const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (at >= (int64_t)p.n_seq * p.stride * p.hq) return;
-    const int64_t row = at / p.hq;
-    const int head = (int)(at - row * p.hq), b = (int)(row / p.stride), r = (int)(row - (int64_t)b * p.stride);
-    const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride), g = p.hq / p.hkv;
-    if (r >= n || S < 0 || (int64_t)S + n > p.max_ctx) return;
-    const int q0 = (r * g + head % g) / kRows * kRows;
-    const int nsplit = (tile_end(S, n * g, q0, g) + p.chunk - 1) / p.chunk;
-    if (nsplit <= 1) return;
-    const float2 ml = lane < nsplit ? __ldcg(p.part_ml + at * p.max_splits + lane) : make_float2(-INFINITY, 0.f);
-    const float m = warp_max(ml.x);
-    const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
-    const float l = warp_sum(w * ml.y);
-    const float wl = l > 0.f || l != l ? w * p.v_scale / l : 0.f;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + lane;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < nsplit; s0 += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-            v[x] = s0 + x < nsplit ? __ldcg(po + (int64_t)(s0 + x) * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const float f = __shfl_sync(0xffffffffu, wl, (s0 + x) & 31);
-            acc.x += f * v[x].x;
-            acc.y += f * v[x].y;
-            acc.z += f * v[x].z;
-            acc.w += f * v[x].w;
-        }
+    if (nsplit == 1) return;
+    // The chunk that finishes last joins them all.  The ticket counts to nsplit
+    // and wraps to zero, so the workspace is as it was.
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        s_last = atomicInc(p.tickets + ((int64_t)b * p.hkv + h) * p.tiles + tile, nsplit - 1) == (unsigned)nsplit - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    for (int r = warp; r < kRows && q0 + r < rows; r += kWarps) {
+        const int qr = q0 + r;
+        join_splits(p, (row0 + qr / g) * p.hq + h * g + qr % g, nsplit, lane);
     }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 // ---------------------------------------------------------------------------
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttnKv4Plan {
-    int chunk, max_splits, tiles;
-    size_t off_ml, off_o, bytes;
+    int nt, chunk, max_splits, tiles;
+    size_t off_ticket, off_ml, off_o, bytes;
 };
 
 bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4Plan* w) {
@@ -624,19 +644,23 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int g = hq / hkv;
-    w->tiles = (stride * g + kRows - 1) / kRows;
+    // One n-tile where a sequence's query rows fit in it.
+    w->nt = stride * g <= 8 ? 1 : 2;
+    w->tiles = (stride * g + 8 * w->nt - 1) / (8 * w->nt);
     // Chunks by the call's capacity alone (a sequence's result does not depend on
-    // its neighbours' lengths): about one item per resident CTA when the
-    // sequences are at half the capacity, 256 to 2048 keys.
+    // its neighbours' lengths): two items per resident CTA when the sequences are
+    // at half the capacity, 512 to 2048 keys.
     const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
     const int64_t blocks = pairs * std::max(1, (max_ctx / 2 + 63) / 64);
-    int64_t cb = (blocks + 3LL * sms - 1) / (3LL * sms);
-    cb = std::max<int64_t>(4, std::min<int64_t>(cb, kMaxChunk / 64));
+    const int64_t items = (w->nt == 1 ? 10LL : 6LL) * sms;
+    int64_t cb = (blocks + items - 1) / items;
+    cb = std::max<int64_t>(8, std::min<int64_t>(cb, kMaxChunk / 64));
     cb = std::max<int64_t>(cb, ((int64_t)max_ctx + 64LL * kMaxSplits - 1) / (64LL * kMaxSplits));
     w->chunk = (int)std::min<int64_t>(cb * 64, 1 << 30);
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
-    w->off_ml = 256;
+    w->off_ticket = 256;
+    w->off_ml = w->off_ticket + (w->max_splits > 1 ? round256((size_t)pairs * sizeof(unsigned)) : 0);
     w->off_o = w->off_ml + round256(parts * sizeof(float2));
     w->bytes = w->off_o + round256(parts * HD * sizeof(float));
     return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
@@ -732,14 +756,12 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     char* ws = static_cast<char*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;
     const AttnKv4Params p{(const bf16*)q, (const uint8_t*)kv4_pool, page_table, S, n, (bf16*)out,
-                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (int*)ws, num_pages, n_heads, n_kv_heads,
-                          pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits, w.tiles, k_scale, v_scale};
-    const int64_t ctas = (int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits;
-    cudaError_t e = launch_pdl(attn_kv4_kernel, dim3((unsigned)ctas), dim3(kWarps * 32), 0, st, p);
-    if (e == cudaSuccess && w.max_splits > 1) {
-        const int64_t pairs = (int64_t)n_seq * stride * n_heads;
-        e = launch_pdl(attn_kv4_merge_kernel, dim3((unsigned)((pairs + 7) / 8)), dim3(256), 0, st, p);
-    }
+                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (unsigned*)(ws + w.off_ticket), (int*)ws,
+                          num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
+                          w.tiles, k_scale, v_scale};
+    const dim3 grid((unsigned)((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits));
+    const cudaError_t e = w.nt == 1 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(kWarps * 32), 0, st, p)
+                                    : launch_pdl(attn_kv4_kernel<2>, grid, dim3(kWarps * 32), 0, st, p);
     return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
 }
 
