@@ -14,6 +14,7 @@
 // tokens x 8 bytes], brought in by one bulk copy.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -222,10 +223,9 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // Attention over the 4-bit cache: out = softmax(q K^T / sqrt(128)) V of window
 // rows r over cache positions 0 .. S + r, as wedlm_attention_bf16.
 //
-// Work item (a CTA of four warps): NT * 8 query rows (window rows x the g
-// heads that share a KV head), one KV head, one chunk of keys; the warps take
-// the chunk's pages in turn, each with its own ring of page buffers filled by
-// bulk copies, and join their results at the end.  Codes go from shared memory
+// Work item (a CTA of one warp): NT * 8 query rows (window rows x the g heads
+// that share a KV head), one KV head, one chunk of keys, two pages at a time
+// through a ring of page buffers filled by bulk copies.  Codes go from shared memory
 // to registers, are widened and scaled there and feed mma.sync directly: no
 // widened copy of K or V is ever written anywhere.  The cache is the M side of
 // both products (S^T = K Q^T, O^T = V^T P^T), so that a token's 4 to 8 query
@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // are permuted inside the products (which changes no sum): in K Q^T the lanes
 // of a quad own 32 consecutive dims each, so a lane's operands of a key are 16
 // consecutive bytes; in V^T P^T a lane owns the 16 dims of one scale block.
+// Warps share nothing, so the SM's schedulers always have others to run while
+// one of them starts, waits or writes its result.
 //
 // Q is held in fp16 scaled per row by a power of two (its largest element in
 // [2^14, 2^15)), which keeps every bit of a bf16 q that is within 2^-28 of the
@@ -240,10 +242,14 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // to a running maximum that is only raised when a score exceeds it by 2^8, and
 // times 2^6, so weights down to 2^-30 of the largest are kept; sums and
 // outputs are fp32.
-constexpr int kWarps = 4;
-constexpr int kStages = 4;
-constexpr int kMaxSplits = 32;
-constexpr int kMaxChunk = 2048;       // keys of a chunk, unless the context needs more per chunk
+constexpr int kWarps = 4;              // items (warps) of a CTA
+constexpr int kStep = 2;              // pages taken together
+constexpr int kStepKeys = kStep * kPage;
+constexpr int kStages = 2;
+constexpr int kMaxSplits = 128;
+constexpr int kMaxChunk = 1024;       // keys of a chunk, unless the context needs more per chunk
+constexpr int kItemsPerSm = 48;
+constexpr int kTicketSplits = 8;      // up to this many chunks the last one to finish joins them
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum tolerated before O is rescaled
 constexpr float kWeightLog2 = 6.0f;   // weights are held times 2^6
 
@@ -270,7 +276,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -286,10 +292,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ void bar_init(uint64_t* bar) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 // One head's page into shared memory; completes on `bar`.
 __device__ __forceinline__ void load_page(void* dst, const uint8_t* src, uint64_t* bar) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(kHeadPage)
-                 : "memory");
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(smem_u32(dst)), "l"(src), "r"(kHeadPage), "r"(smem_u32(bar)) : "memory");
 }
@@ -320,103 +330,120 @@ __device__ __forceinline__ int load_q(const bf16* q, bool live, uint32_t (&a)[16
     return e;
 }
 
-// The 16 rows of chunk results of one (row, head) joined and written; lane s
-// holds chunk s's (m, l), a lane writes four dims.
-__device__ __forceinline__ void join_splits(const AttnKv4Params& p, int64_t at, int nsplit, int lane) {
-    const float2 ml = lane < nsplit ? __ldcg(p.part_ml + at * p.max_splits + lane) : make_float2(-INFINITY, 0.f);
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + lane;
+__device__ __forceinline__ void store_out(const AttnKv4Params& p, int64_t at, int lane, float4 v, float f) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// What the outputs are multiplied by, given the weights' sum: 0 for a row that
+// saw no key (every page of it outside the pool), NaN where the sum is.
+__device__ __forceinline__ float out_factor(float v_scale, float l) { return l > 0.f || l != l ? v_scale / l : 0.f; }
+
+// Chunks s0 .. s0 + 31 of one (row, head), those below `end`: weights relative
+// to their common maximum m, in lane s - s0; the weighted sum of the outputs'
+// dims 4 lane .. + 3 in acc and of the l's in l.
+__device__ __forceinline__ void join_range(const AttnKv4Params& p, int64_t at, int s0, int end, int lane, float& m,
+                                           float& l, float4& acc) {
+    const int count = min(32, end - s0);
+    const float2 ml = lane < count ? __ldcg(p.part_ml + at * p.max_splits + s0 + lane) : make_float2(-INFINITY, 0.f);
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + (at * p.max_splits + s0) * HD) + lane;
     float4 v[8];
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
-        v[x] = x < nsplit ? __ldcg(po + (int64_t)x * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    const float m = warp_max(ml.x);
+    for (int x = 0; x < 8; ++x) v[x] = x < count ? __ldcg(po + x * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    m = warp_max(ml.x);
     const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - m);
-    const float l = warp_sum(w * ml.y);
-    const float wl = l > 0.f || l != l ? w * p.v_scale / l : 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < nsplit; s0 += 8) {
-        if (s0 > 0) {
+    l = warp_sum(w * ml.y);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < count; x0 += 8) {
+        if (x0 > 0) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                v[x] = s0 + x < nsplit ? __ldcg(po + (int64_t)(s0 + x) * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[x] = x0 + x < count ? __ldcg(po + (x0 + x) * (HD / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const float f = __shfl_sync(0xffffffffu, wl, (s0 + x) & 31);
+            const float f = __shfl_sync(0xffffffffu, w, (x0 + x) & 31);
             acc.x += f * v[x].x;
             acc.y += f * v[x].y;
             acc.z += f * v[x].z;
             acc.w += f * v[x].w;
         }
     }
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 3) attn_kv4_kernel(const AttnKv4Params p) {
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(const AttnKv4Params p) {
     constexpr int kRows = 8 * NT;
-    __shared__ __align__(128) uint8_t ring[kWarps][kStages][kHeadPage];
-    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
-    __shared__ float2 s_ml[kWarps][kRows];
-    __shared__ int s_last;
+    __shared__ __align__(128) uint8_t rings[kWarps][kStages][kStep][kHeadPage];
+    __shared__ __align__(8) uint64_t all_bars[kWarps][kStages];
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, j8 = lane >> 2;
+    auto& ring = rings[warp];
+    uint64_t* bars = all_bars[warp];
     const int g = p.hq / p.hkv;
-    int64_t id = blockIdx.x;
+    int64_t id = (int64_t)blockIdx.x * kWarps + warp;
     const int tile = (int)(id % p.tiles);
     id /= p.tiles;
     const int sp = (int)(id % p.max_splits);
     id /= p.max_splits;
     const int h = (int)(id % p.hkv), b = (int)(id / p.hkv);
+    if (b >= p.n_seq) return;
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
     const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
     const int ks = sp * p.chunk, page0 = ks / kPage;
-    // Page ids of this warp's pages, 32 at a time, one per lane; the first ones
-    // are read together with S and n.
-    auto raw_id = [&](int k) {
-        const int idx = page0 + warp + k * kWarps;
-        return idx < p.pages_per_seq && k * kWarps * kPage < p.chunk ? __ldcg(table + idx) : -1;
-    };
+    // Page ids, 32 at a time, one per lane; the first ones are read together with S and n.
+    auto raw_id = [&](int k) { return page0 + k < p.pages_per_seq && k * kPage < p.chunk ? __ldcg(table + page0 + k) : -1; };
     int ids = raw_id(lane);
     if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) bar_init(&bars[warp][s]);
+        for (int s = 0; s < kStages; ++s) bar_init(&bars[s]);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
     const int rows = n * g, q0 = tile * kRows;
     if (n <= 0 || q0 >= rows) return;
     if (S < 0 || (int64_t)S + n > p.max_ctx) {
-        if (threadIdx.x == 0) set_error(p.err, kErrBounds);
+        set_error(p.err, kErrBounds);
         return;
     }
     const int kend = S + (min(q0 + kRows, rows) - 1) / g + 1;
     const int nsplit = (kend + p.chunk - 1) / p.chunk;
     if (sp >= nsplit) return;
     const int ke = min(kend, ks + p.chunk);
-    const int npages = (ke + kPage - 1) / kPage - page0;
-    const int mine = npages > warp ? (npages - warp + kWarps - 1) / kWarps : 0;  // pages of this warp
-    // Load k of this warp into its stage; a page outside the pool is not loaded
-    // and its keys count as masked.
-    uint32_t have = 0;  // bit s: the page in stage s was loaded
+    const int npages = (ke + kPage - 1) / kPage - page0, steps = (npages + kStep - 1) / kStep;
+    // Step k's pages into its stage; a page outside the pool is not loaded and
+    // its keys count as masked.
+    uint32_t gone = 0;  // bit kStep * s + x: page x of stage s is not there
     int issued = 0;
     auto issue = [&]() {
-        if ((issued & 31) == 0 && issued > 0) ids = raw_id(issued + lane);
-        const int page = __shfl_sync(0xffffffffu, ids, issued & 31);
-        const int s = issued % kStages;
-        have &= ~(1u << s);
-        if (page >= 0 && page < p.num_pages) {
-            have |= 1u << s;
-            if (lane == 0)
-                load_page(ring[warp][s], p.pool + ((int64_t)page * p.hkv + h) * kHeadPage, &bars[warp][s]);
-        } else {
-            set_error(p.err, kErrBounds);
+        const int k0 = issued * kStep, s = issued % kStages;
+        if ((k0 & 31) == 0 && k0 > 0) ids = raw_id(k0 + lane);
+        int page[kStep];
+        uint32_t bytes = 0;
+        gone &= ~(((1u << kStep) - 1) << (kStep * s));
+#pragma unroll
+        for (int x = 0; x < kStep; ++x) {
+            page[x] = __shfl_sync(0xffffffffu, ids, (k0 + x) & 31);
+            const bool wanted = k0 + x < npages;
+            if (wanted && page[x] >= 0 && page[x] < p.num_pages) {
+                bytes += kHeadPage;
+            } else {
+                if (wanted) set_error(p.err, kErrBounds);
+                gone |= 1u << (kStep * s + x);
+                page[x] = -1;
+            }
+        }
+        if (lane == 0) {
+            bar_expect(&bars[s], bytes);
+#pragma unroll
+            for (int x = 0; x < kStep; ++x)
+                if (page[x] >= 0)
+                    load_page(ring[s][x], p.pool + ((int64_t)page[x] * p.hkv + h) * kHeadPage, &bars[s]);
         }
         ++issued;
     };
-    while (issued < min(mine, kStages)) issue();
+    while (issued < min(steps, kStages)) issue();
 
     // Q of row j8 of every n-tile (operand B) and, for the lane's own columns
     // (queries 2c and 2c + 1 of every n-tile), score factors and last keys
@@ -441,95 +468,74 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 3) attn_kv4_kernel(
     lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, 2));
 
     float o[8][NT][4] = {};
-    float m[NT][2], l[NT][2] = {};  // maxima in the exp2 domain
+    // Per own column: the running maximum m of the scores in the exp2 domain and
+    // the weights' sum; a weight is exp2(score + z), z = 6 - m (huge before the
+    // first key, so that any visible key raises the maximum).
+    float m[NT][2], z[NT][2], l[NT][2] = {};
 #pragma unroll
-    for (int t = 0; t < NT; ++t) m[t][0] = m[t][1] = -INFINITY;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int k = 0; k < mine; ++k) {
-        const int s = k % kStages;
-        if ((have >> s) & 1) {
-            ok = mbar_wait_bounded(smem_u32(&bars[warp][s]), (phase >> s) & 1, p.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            phase ^= 1u << s;
-            const uint8_t* K = ring[warp][s];
-            const uint8_t* V = K + kHalfPage;
-            const int key0 = (page0 + warp + k * kWarps) * kPage;
-            const bool edge = key0 + kPage - 1 > lim_min;
-            // S^T of the page's 16 keys: lane's rows are keys j8 and j8 + 8
-            float sc[NT][4] = {};
-            {
-                const uint4 u0 = *reinterpret_cast<const uint4*>(K + j8 * 64 + c * 16);
-                const uint4 u1 = *reinterpret_cast<const uint4*>(K + (j8 + 8) * 64 + c * 16);
-                const uint32_t s0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + c * 2));
-                const uint32_t s1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + 64 + c * 2));
-                const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-                const uint32_t f0[2] = {__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)};
-                const uint32_t f1[2] = {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)};
+    for (int t = 0; t < NT; ++t) {
+        m[t][0] = m[t][1] = -INFINITY;
+        z[t][0] = z[t][1] = 1e30f;
+    }
+    // kStep pages from key0 on; `edge`: some of the keys are not visible to some row,
+    // or (bits of `out`) a page is not there.
+    auto step = [&](const uint8_t* base_page, int key0, uint32_t out, auto edge_) {
+        constexpr bool edge = decltype(edge_)::value;
+        // S^T: lane's rows are keys j8 and j8 + 8 of each page
+        float sc[kStep][NT][4] = {};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t a[4], d[4];
-                    e2m1x8_to_f16x2(w0[x], a);
-                    e2m1x8_to_f16x2(w1[x], d);
+        for (int pg = 0; pg < kStep; ++pg) {
+            const uint8_t* K = base_page + pg * kHeadPage;
+            const uint4 u0 = *reinterpret_cast<const uint4*>(K + j8 * 64 + c * 16);
+            const uint4 u1 = *reinterpret_cast<const uint4*>(K + j8 * 64 + 512 + c * 16);
+            const uint32_t s0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + c * 2));
+            const uint32_t s1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + 64 + c * 2));
+            const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
+            const uint32_t f0[2] = {__byte_perm(s0, s0, 0x1010), __byte_perm(s0, s0, 0x3232)};
+            const uint32_t f1[2] = {__byte_perm(s1, s1, 0x1010), __byte_perm(s1, s1, 0x3232)};
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint32_t a0 = hmul2(a[2 * y], f0[x >> 1]), a1 = hmul2(d[2 * y], f1[x >> 1]);
-                        const uint32_t a2 = hmul2(a[2 * y + 1], f0[x >> 1]), a3 = hmul2(d[2 * y + 1], f1[x >> 1]);
+            for (int x = 0; x < 4; ++x) {
+                uint32_t a[4], d[4];
+                e2m1x8_to_f16x2(w0[x], a);
+                e2m1x8_to_f16x2(w1[x], d);
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-                            mma_f16(sc[t], a0, a1, a2, a3, qf[t][4 * x + 2 * y], qf[t][4 * x + 2 * y + 1]);
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t a0 = hmul2(a[2 * y], f0[x >> 1]), a1 = hmul2(d[2 * y], f1[x >> 1]);
+                    const uint32_t a2 = hmul2(a[2 * y + 1], f0[x >> 1]), a3 = hmul2(d[2 * y + 1], f1[x >> 1]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        mma_f16(sc[pg][t], a0, a1, a2, a3, qf[t][4 * x + 2 * y], qf[t][4 * x + 2 * y + 1]);
                 }
             }
-            // V^T: lane's rows are dims 16 j8 .. + 15, its columns keys 2c, 2c + 1, 8 + 2c, 9 + 2c
-            uint32_t vf[2][16];
+        }
+        float top = -INFINITY;
+        float e[kStep][NT][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int tok = t * 8 + 2 * c;
-                const uint2 u0 = *reinterpret_cast<const uint2*>(V + tok * 64 + j8 * 8);
-                const uint2 u1 = *reinterpret_cast<const uint2*>(V + tok * 64 + 64 + j8 * 8);
-                uint32_t b0 = V[kCodes + tok * 8 + j8], b1 = V[kCodes + tok * 8 + 8 + j8];
-                if (edge) {  // keys past the last row's: whatever their bytes say, they add nothing
-                    if (key0 + tok >= ke) b0 = 0;
-                    if (key0 + tok + 1 >= ke) b1 = 0;
+        for (int pg = 0; pg < kStep; ++pg)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (edge && (key0 + pg * kPage + j8 + 8 * (x >> 1) > lim[t][x & 1] || ((out >> pg) & 1)))
+                        sc[pg][t][x] = -INFINITY;
+                    e[pg][t][x] = fmaf(sc[pg][t][x], sl[t][x & 1], z[t][x & 1]);
+                    top = fmaxf(top, e[pg][t][x]);
                 }
-                const uint32_t s2 = e4m3x2_to_f16x2(b0 | b1 << 8);
+        if (__any_sync(0xffffffffu, top > kWeightLog2 + kLazyLog2)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    // bytes of (key, key + 1) codes: even dims, then odd dims
-                    const uint32_t w0 = x ? u0.y : u0.x, w1 = x ? u1.y : u1.x;
-                    const uint32_t ev = (w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u);
-                    const uint32_t od = ((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u);
-                    uint32_t f[4];
-                    e2m1x8_to_f16x2(ev, f);
+                    float v = -INFINITY;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) vf[t][8 * x + 2 * y] = hmul2(f[y], s2);
-                    e2m1x8_to_f16x2(od, f);
+                    for (int pg = 0; pg < kStep; ++pg)
+                        v = fmaxf(v, fmaxf(sc[pg][t][x] * sl[t][x], sc[pg][t][2 + x] * sl[t][x]));
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) vf[t][8 * x + 2 * y + 1] = hmul2(f[y], s2);
-                }
-            }
-            bool grew = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    sc[t][x] *= sl[t][x & 1];
-                    if (edge && key0 + j8 + 8 * (x >> 1) > lim[t][x & 1]) sc[t][x] = -INFINITY;
-                }
-                grew |= fmaxf(sc[t][0], sc[t][2]) > m[t][0] + kLazyLog2 || fmaxf(sc[t][1], sc[t][3]) > m[t][1] + kLazyLog2;
-            }
-            if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float v = fmaxf(sc[t][x], sc[t][2 + x]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                        const float f = v > m[t][x] ? exp2_fast(m[t][x] - v) : 1.f;
-                        m[t][x] = fmaxf(m[t][x], v);
+                    for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                    if (v > m[t][x]) {
+                        const float f = exp2_fast(m[t][x] - v);
+                        m[t][x] = v;
+                        z[t][x] = kWeightLog2 - v;
                         l[t][x] *= f;
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
@@ -537,28 +543,80 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 3) attn_kv4_kernel(
                             o[u][t][2 + x] *= f;
                         }
                     }
-            }
+#pragma unroll
+                    for (int pg = 0; pg < kStep; ++pg) {
+                        e[pg][t][x] = fmaf(sc[pg][t][x], sl[t][x], z[t][x]);
+                        e[pg][t][2 + x] = fmaf(sc[pg][t][2 + x], sl[t][x], z[t][x]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int pg = 0; pg < kStep; ++pg) {
+            uint32_t bt[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float z = m[t][x & 1] == -INFINITY ? 0.f : kWeightLog2 - m[t][x & 1];
-                    sc[t][x] = exp2_fast(sc[t][x] + z);
-                    l[t][x & 1] += sc[t][x];
+                    e[pg][t][x] = exp2_fast(e[pg][t][x]);
+                    l[t][x & 1] += e[pg][t][x];
                 }
-                const uint32_t b0 = transpose8x8(pack_half2(sc[t][0], sc[t][1]));
-                const uint32_t b1 = transpose8x8(pack_half2(sc[t][2], sc[t][3]));
+                bt[t][0] = transpose8x8(pack_half2(e[pg][t][0], e[pg][t][1]));
+                bt[t][1] = transpose8x8(pack_half2(e[pg][t][2], e[pg][t][3]));
+            }
+            // V^T: lane's rows are dims 16 j8 .. + 15, its columns keys 2c, 2c + 1, 8 + 2c, 9 + 2c
+            const uint8_t* V = base_page + pg * kHeadPage + kHalfPage;
+            uint2 u[4];
+            uint32_t s2[2];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    mma_f16(o[u][t], vf[0][2 * u], vf[0][2 * u + 1], vf[1][2 * u], vf[1][2 * u + 1], b0, b1);
+            for (int t = 0; t < 2; ++t) {
+                const int tok = t * 8 + 2 * c;
+                u[2 * t] = *reinterpret_cast<const uint2*>(V + tok * 64 + j8 * 8);
+                u[2 * t + 1] = *reinterpret_cast<const uint2*>(V + tok * 64 + 64 + j8 * 8);
+                uint32_t b0 = V[kCodes + tok * 8 + j8], b1 = V[kCodes + tok * 8 + 8 + j8];
+                if (edge) {  // keys past the last row's: whatever their bytes say, they add nothing
+                    if (key0 + pg * kPage + tok >= ke || ((out >> pg) & 1)) b0 = 0;
+                    if (key0 + pg * kPage + tok + 1 >= ke || ((out >> pg) & 1)) b1 = 0;
+                }
+                s2[t] = e4m3x2_to_f16x2(b0 | b1 << 8);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                // bytes of (key, key + 1) codes: even dims, then odd dims, of 8 dims
+                uint32_t ev[2][4], od[2][4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t w0 = x ? u[2 * t].y : u[2 * t].x, w1 = x ? u[2 * t + 1].y : u[2 * t + 1].x;
+                    e2m1x8_to_f16x2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), ev[t]);
+                    e2m1x8_to_f16x2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), od[t]);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t a0 = hmul2(ev[0][y], s2[0]), a1 = hmul2(od[0][y], s2[0]);
+                    const uint32_t a2 = hmul2(ev[1][y], s2[1]), a3 = hmul2(od[1][y], s2[1]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_f16(o[4 * x + y][t], a0, a1, a2, a3, bt[t][0], bt[t][1]);
+                }
             }
         }
+    };
+    bool ok = true;  // after a wait that gave up the rest is computed from whatever is there: the error word tells
+    for (int k = 0, s = 0, par = 0; k < steps; ++k) {
+        const int key0 = (page0 + k * kStep) * kPage;
+        ok = mbar_wait_bounded(smem_u32(&bars[s]), par, p.err) && ok;
+        __syncwarp();
+        const uint32_t out = (gone >> (kStep * s)) & ((1u << kStep) - 1);
+        if (key0 + kStepKeys - 1 > lim_min || out) step(ring[s][0], key0, out, std::true_type());
+        else step(ring[s][0], key0, 0, std::false_type());
         __syncwarp();  // every lane has read the stage
-        if (issued < mine) issue();
+        if (issued < steps) issue();
+        if (++s == kStages) {
+            s = 0;
+            par ^= 1;
+        }
     }
-    if (!ok) {  // copies still in flight land before the CTA's memory is given up
-        for (int s = 0; s < kStages; ++s)
-            if ((have >> s) & 1) mbar_wait_bounded(smem_u32(&bars[warp][s]), (phase >> s) & 1, nullptr, 200000000LL);
+    if (__any_sync(0xffffffffu, !ok)) {  // copies still in flight land before the CTA's memory is given up
+        for (int k = max(0, steps - kStages); k < steps; ++k)
+            mbar_wait_bounded(smem_u32(&bars[k % kStages]), (k / kStages) & 1, nullptr, 200000000LL);
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -566,67 +624,80 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 5 : 3) attn_kv4_kernel(
         for (int x = 0; x < 2; ++x) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], d);
-            if (j8 == 0) s_ml[warp][8 * t + 2 * c + x] = make_float2(m[t][x], l[t][x]);
+            // dims 16 j8 .. + 15 of the column's row
+            const int qr = q0 + 8 * t + 2 * c + x;
+            if (qr >= rows) continue;
+            const int64_t at = (row0 + qr / g) * p.hq + h * g + qr % g;
+            if (nsplit == 1) {
+                const float f = out_factor(p.v_scale, l[t][x]);
+#pragma unroll
+                for (int u = 0; u < 8; u += 2)
+                    store_out(p, at, 4 * j8 + u / 2,
+                              make_float4(o[u][t][x], o[u][t][2 + x], o[u + 1][t][x], o[u + 1][t][2 + x]), f);
+            } else {
+                float4* dst = reinterpret_cast<float4*>(p.part_o + (at * p.max_splits + sp) * HD + 16 * j8);
+#pragma unroll
+                for (int u = 0; u < 8; u += 2)
+                    dst[u / 2] = make_float4(o[u][t][x], o[u][t][2 + x], o[u + 1][t][x], o[u + 1][t][2 + x]);
+                if (j8 == 0) p.part_ml[at * p.max_splits + sp] = make_float2(m[t][x], l[t][x]);
+            }
         }
-    // join the warps: O through the rings' memory
-    __syncthreads();
-    constexpr int kPad = HD + 4;
-    float* so = reinterpret_cast<float*>(&ring[0][0][0]);  // [kWarps][kRows][kPad]
-    static_assert(kWarps * kRows * kPad * 4 <= (int)sizeof(ring), "O of every warp fits in the rings");
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float* dst = so + (warp * kRows + 8 * t + 2 * c + x) * kPad + 16 * j8;
-#pragma unroll
-            for (int u = 0; u < 8; u += 2)
-                *reinterpret_cast<float4*>(dst + 2 * u) =
-                    make_float4(o[u][t][x], o[u][t][2 + x], o[u + 1][t][x], o[u + 1][t][2 + x]);
-        }
-    __syncthreads();
-    for (int r = warp; r < kRows && q0 + r < rows; r += kWarps) {
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_ml[w][r].x);
-        float ll = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = s_ml[w][r].x == -INFINITY ? 0.f : exp2_fast(s_ml[w][r].x - mm);
-            ll += f * s_ml[w][r].y;
-            const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * kPad + 4 * lane);
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
-        }
-        const int qr = q0 + r;
-        const int64_t at = (row0 + qr / g) * p.hq + h * g + qr % g;
-        if (nsplit == 1) {
-            const float inv = ll > 0.f || ll != ll ? p.v_scale / ll : 0.f;
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        } else {
-            *reinterpret_cast<float4*>(p.part_o + (at * p.max_splits + sp) * HD + 4 * lane) = acc;
-            if (lane == 0) p.part_ml[at * p.max_splits + sp] = make_float2(mm, ll);
-        }
-    }
-    if (nsplit == 1) return;
+    if (nsplit == 1 || p.max_splits > kTicketSplits) return;
     // The chunk that finishes last joins them all.  The ticket counts to nsplit
     // and wraps to zero, so the workspace is as it was.
     __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0)
-        s_last = atomicInc(p.tickets + ((int64_t)b * p.hkv + h) * p.tiles + tile, nsplit - 1) == (unsigned)nsplit - 1;
-    __syncthreads();
-    if (!s_last) return;
+    __syncwarp();
+    unsigned last = 0;
+    if (lane == 0)
+        last = atomicInc(p.tickets + ((int64_t)b * p.hkv + h) * p.tiles + tile, nsplit - 1) == (unsigned)nsplit - 1;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
-    for (int r = warp; r < kRows && q0 + r < rows; r += kWarps) {
-        const int qr = q0 + r;
-        join_splits(p, (row0 + qr / g) * p.hq + h * g + qr % g, nsplit, lane);
+    for (int r = q0; r < min(q0 + kRows, rows); ++r) {
+        const int64_t at = (row0 + r / g) * p.hq + h * g + r % g;
+        float mm, ll;
+        float4 acc;
+        join_range(p, at, 0, nsplit, lane, mm, ll, acc);
+        store_out(p, at, lane, acc, out_factor(p.v_scale, ll));
     }
+}
+
+// The key chunks of a (row, query head) joined, where they are many: a CTA
+// each, a warp for every 32 chunks.
+__global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4Params p, int tile_rows) {
+    __shared__ float4 s_acc[kMaxSplits / 32][32];
+    __shared__ float2 s_ml[kMaxSplits / 32];
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t at = blockIdx.x;
+    const int64_t row = at / p.hq;
+    const int head = (int)(at - row * p.hq), b = (int)(row / p.stride), r = (int)(row - (int64_t)b * p.stride);
+    const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride), g = p.hq / p.hkv;
+    if (r >= n || S < 0 || (int64_t)S + n > p.max_ctx) return;
+    const int q_end = min(((r * g + head % g) / tile_rows + 1) * tile_rows, n * g);
+    const int nsplit = (S + (q_end - 1) / g + 1 + p.chunk - 1) / p.chunk;
+    if (nsplit <= 1) return;
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (32 * warp < nsplit) join_range(p, at, 32 * warp, nsplit, lane, m, l, acc);
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp > 0) return;
+    const int parts = blockDim.x >> 5;
+    for (int w = 0; w < parts; ++w) m = fmaxf(m, s_ml[w].x);
+    l = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < parts; ++w) {
+        const float f = s_ml[w].x == -INFINITY ? 0.f : exp2_fast(s_ml[w].x - m);
+        const float4 v = s_acc[w][lane];
+        l += f * s_ml[w].y;
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+    }
+    store_out(p, at, lane, acc, out_factor(p.v_scale, l));
 }
 
 // ---------------------------------------------------------------------------
@@ -648,19 +719,18 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     w->nt = stride * g <= 8 ? 1 : 2;
     w->tiles = (stride * g + 8 * w->nt - 1) / (8 * w->nt);
     // Chunks by the call's capacity alone (a sequence's result does not depend on
-    // its neighbours' lengths): two items per resident CTA when the sequences are
-    // at half the capacity, 512 to 2048 keys.
+    // its neighbours' lengths): kItemsPerSm items for every SM when the sequences
+    // are at half the capacity, 64 to 1024 keys.
     const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
-    const int64_t blocks = pairs * std::max(1, (max_ctx / 2 + 63) / 64);
-    const int64_t items = (w->nt == 1 ? 10LL : 6LL) * sms;
-    int64_t cb = (blocks + items - 1) / items;
-    cb = std::max<int64_t>(8, std::min<int64_t>(cb, kMaxChunk / 64));
-    cb = std::max<int64_t>(cb, ((int64_t)max_ctx + 64LL * kMaxSplits - 1) / (64LL * kMaxSplits));
-    w->chunk = (int)std::min<int64_t>(cb * 64, 1 << 30);
+    const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)kItemsPerSm * sms;
+    int64_t cb = ((keys + items - 1) / items + kStepKeys - 1) / kStepKeys;
+    cb = std::max<int64_t>(64 / kStepKeys, std::min<int64_t>(cb, kMaxChunk / kStepKeys));
+    cb = std::max<int64_t>(cb, ((int64_t)max_ctx + (int64_t)kStepKeys * kMaxSplits - 1) / ((int64_t)kStepKeys * kMaxSplits));
+    w->chunk = (int)std::min<int64_t>(cb * kStepKeys, 1 << 30);
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
     w->off_ticket = 256;
-    w->off_ml = w->off_ticket + (w->max_splits > 1 ? round256((size_t)pairs * sizeof(unsigned)) : 0);
+    w->off_ml = w->off_ticket + (w->max_splits > 1 && w->max_splits <= kTicketSplits ? round256((size_t)pairs * sizeof(unsigned)) : 0);
     w->off_o = w->off_ml + round256(parts * sizeof(float2));
     w->bytes = w->off_o + round256(parts * HD * sizeof(float));
     return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
@@ -759,9 +829,12 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
                           (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (unsigned*)(ws + w.off_ticket), (int*)ws,
                           num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
                           w.tiles, k_scale, v_scale};
-    const dim3 grid((unsigned)((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits));
-    const cudaError_t e = w.nt == 1 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(kWarps * 32), 0, st, p)
-                                    : launch_pdl(attn_kv4_kernel<2>, grid, dim3(kWarps * 32), 0, st, p);
+    const dim3 grid((unsigned)(((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits + kWarps - 1) / kWarps));
+    cudaError_t e = w.nt == 1 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32 * kWarps), 0, st, p)
+                              : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32 * kWarps), 0, st, p);
+    if (e == cudaSuccess && w.max_splits > kTicketSplits)
+        e = launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((int64_t)n_seq * stride * n_heads)),
+                       dim3((w.max_splits + 31) / 32 * 32), 0, st, p, 8 * w.nt);
     return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
 }
 
