@@ -16,8 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "wedlm")
 LIB = os.path.join(HERE, "libwedlm.so")
-SOURCES = ["kernels.cu", "gemm_tc.cu", "attn_tc.cu", "wedlm.cu", "standalone.cu", "noalloc.cu", "kv4.cu", "kv_pages.cu"]
-HEADERS = ["common.cuh", "kernels.cuh", "gemm_tc.cuh"]
+SOURCES = ["kernels.cu", "gemm_tc.cu", "attn_tc.cu", "wedlm.cu", "standalone.cu", "noalloc.cu", "kv4.cu", "kv4_tc.cu", "kv_pages.cu"]
+HEADERS = ["common.cuh", "kernels.cuh", "gemm_tc.cuh", "kv4.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

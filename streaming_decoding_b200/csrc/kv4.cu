@@ -1,68 +1,15 @@
 // A KV cache held in 4 bits and the attention that reads it.
 //
-// Format.  A row of 128 dims (one token's K or V of one head) is 8 blocks of
-// 16 dims; a block is one scale s (e4m3) and 16 codes (e2m1: +-{0, .5, 1, 1.5,
-// 2, 3, 4, 6}), and stands for code * s * k_scale (or v_scale), the latter a
-// power of two the caller chooses.  4.5 bits per value, against 16.
-//   s = e4m3(max|x| / 6),  code = e2m1(x / s),  both rounded to nearest even.
-// A code has 2 and a scale 4 significant bits, so code * s is exact in fp16
-// (at most 6 * 448, at least 2^-10): the attention multiplies them in fp16 and
-// feeds the tensor cores without any rounding.
-//
-// A page of one head is 2304 contiguous bytes: [K, V][codes: 16 tokens x 64
-// bytes (dim 2i in the low, 2i + 1 in the high nibble of byte i)][scales: 16
-// tokens x 8 bytes], brought in by one bulk copy.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
-#include <cuda_fp16.h>
-
-#include "kernels.cuh"
+#include "kv4.cuh"
 
 namespace wedlm {
 namespace {
 
-constexpr int HD = 128;
-constexpr int kHalfPage = WEDLM_KV4_HALF_PAGE;  // K or V of one head's page
-constexpr int kHeadPage = 2 * kHalfPage;  // both
-constexpr int kCodes = kPage * HD / 2;    // bytes of codes in a half page
-
-// ---------------------------------------------------------------------------
-// Conversions between fp32 / fp16 and the 4- and 8-bit formats (one
-// instruction each on sm_100a).
-// The four bytes of a word: eight values.
-__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&r)[4]) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(two));
-    return r;
-}
-__device__ __forceinline__ uint32_t f32_to_e2m1x2(float lo, float hi) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 a, z;\n\tmov.b16 {z, z}, 0;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-        "mov.b32 %0, {a, z, z, z};\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
-    return r & 0xFFu;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ float2 half2_floats(uint32_t a) { return __half22float2(*reinterpret_cast<__half2*>(&a)); }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&r);
-}
+using namespace kv4;
 
 // ---------------------------------------------------------------------------
 // Rows in and out of the cache.
@@ -246,33 +193,9 @@ constexpr int kWarps = 4;              // items (warps) of a CTA
 constexpr int kStep = 2;              // pages taken together
 constexpr int kStepKeys = kStep * kPage;
 constexpr int kStages = 2;
-constexpr int kMaxSplits = 128;
-constexpr int kMaxChunk = 1024;       // keys of a chunk, unless the context needs more per chunk
 constexpr int kItemsPerSm = 48;
+constexpr int kItemsPerSmTc = 6;
 constexpr int kTicketSplits = 8;      // up to this many chunks the last one to finish joins them
-constexpr float kLazyLog2 = 8.0f;     // growth of the maximum tolerated before O is rescaled
-constexpr float kWeightLog2 = 6.0f;   // weights are held times 2^6
-
-struct AttnKv4Params {
-    const bf16* q;
-    const uint8_t* pool;
-    const int32_t* table;
-    const int32_t* S;
-    const int32_t* n;
-    bf16* out;
-    float* part_o;       // [rows][hq][max_splits][128]
-    float2* part_ml;     // [rows][hq][max_splits]
-    unsigned* tickets;   // [n_seq][hkv][tiles], zero between calls
-    int* err;
-    int num_pages, hq, hkv, pages_per_seq, n_seq, stride, max_ctx, chunk, max_splits, tiles;
-    float k_scale, v_scale;
-};
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -287,21 +210,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-
-__device__ __forceinline__ void bar_init(uint64_t* bar) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-// One head's page into shared memory; completes on `bar`.
-__device__ __forceinline__ void load_page(void* dst, const uint8_t* src, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                 ::"r"(smem_u32(dst)), "l"(src), "r"(kHeadPage), "r"(smem_u32(bar)) : "memory");
 }
 
 // A lane's 32 dims of one query row (32 c .. 32 c + 31), scaled to fp16: the
@@ -335,10 +243,6 @@ __device__ __forceinline__ void store_out(const AttnKv4Params& p, int64_t at, in
     *reinterpret_cast<uint2*>(p.out + at * HD + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
-
-// What the outputs are multiplied by, given the weights' sum: 0 for a row that
-// saw no key (every page of it outside the pool), NaN where the sum is.
-__device__ __forceinline__ float out_factor(float v_scale, float l) { return l > 0.f || l != l ? v_scale / l : 0.f; }
 
 // Chunks s0 .. s0 + 31 of one (row, head), those below `end`: weights relative
 // to their common maximum m, in lane s - s0; the weighted sum of the outputs'
@@ -663,7 +567,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
 
 // The key chunks of a (row, query head) joined, where they are many: a CTA
 // each, a warp for every 32 chunks.
-__global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4Params p, int tile_rows) {
+__global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4Params p) {
     __shared__ float4 s_acc[kMaxSplits / 32][32];
     __shared__ float2 s_ml[kMaxSplits / 32];
     griddep_wait();
@@ -674,7 +578,7 @@ __global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4
     const int head = (int)(at - row * p.hq), b = (int)(row / p.stride), r = (int)(row - (int64_t)b * p.stride);
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride), g = p.hq / p.hkv;
     if (r >= n || S < 0 || (int64_t)S + n > p.max_ctx) return;
-    const int q_end = min(((r * g + head % g) / tile_rows + 1) * tile_rows, n * g);
+    const int q_end = min(((r * g + head % g) / p.tile_rows + 1) * p.tile_rows, n * g);
     const int nsplit = (S + (q_end - 1) / g + 1 + p.chunk - 1) / p.chunk;
     if (nsplit <= 1) return;
     float m = -INFINITY, l = 0.f;
@@ -704,7 +608,7 @@ __global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttnKv4Plan {
-    int nt, chunk, max_splits, tiles;
+    int tile_rows, chunk, max_splits, tiles, sms;
     size_t off_ticket, off_ml, off_o, bytes;
 };
 
@@ -714,23 +618,26 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int g = hq / hkv;
-    // One n-tile where a sequence's query rows fit in it.
-    w->nt = stride * g <= 8 ? 1 : 2;
-    w->tiles = (stride * g + 8 * w->nt - 1) / (8 * w->nt);
+    w->sms = sms;
+    // Tiles of 8 or 16 query rows (kv4.cu), of 128 or 256 (kv4_tc.cu): the
+    // smallest that holds a sequence's.
+    const int rows = stride * (hq / hkv);
+    w->tile_rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+    w->tiles = (rows + w->tile_rows - 1) / w->tile_rows;
+    const bool tc = w->tile_rows > 16;
     // Chunks by the call's capacity alone (a sequence's result does not depend on
-    // its neighbours' lengths): kItemsPerSm items for every SM when the sequences
-    // are at half the capacity, 64 to 1024 keys.
+    // its neighbours' lengths): some items for every SM when the sequences are at
+    // half the capacity, and not so short that starting an item shows.
     const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
-    const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)kItemsPerSm * sms;
-    int64_t cb = ((keys + items - 1) / items + kStepKeys - 1) / kStepKeys;
-    cb = std::max<int64_t>(64 / kStepKeys, std::min<int64_t>(cb, kMaxChunk / kStepKeys));
-    cb = std::max<int64_t>(cb, ((int64_t)max_ctx + (int64_t)kStepKeys * kMaxSplits - 1) / ((int64_t)kStepKeys * kMaxSplits));
-    w->chunk = (int)std::min<int64_t>(cb * kStepKeys, 1 << 30);
+    const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)(tc ? kItemsPerSmTc : kItemsPerSm) * sms;
+    const int64_t unit = 64, least = tc ? 256 : 64, most = tc ? 2048 : 1024;
+    int64_t chunk = std::max(least, std::min(most, ((keys + items - 1) / items + unit - 1) / unit * unit));
+    chunk = std::max(chunk, ((int64_t)max_ctx + unit * kMaxSplits - 1) / (unit * kMaxSplits) * unit);
+    w->chunk = (int)std::min<int64_t>(chunk, 1 << 30);
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
     w->off_ticket = 256;
-    w->off_ml = w->off_ticket + (w->max_splits > 1 && w->max_splits <= kTicketSplits ? round256((size_t)pairs * sizeof(unsigned)) : 0);
+    w->off_ml = w->off_ticket + (!tc && w->max_splits > 1 && w->max_splits <= kTicketSplits ? round256((size_t)pairs * sizeof(unsigned)) : 0);
     w->off_o = w->off_ml + round256(parts * sizeof(float2));
     w->bytes = w->off_o + round256(parts * HD * sizeof(float));
     return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
@@ -828,13 +735,15 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     const AttnKv4Params p{(const bf16*)q, (const uint8_t*)kv4_pool, page_table, S, n, (bf16*)out,
                           (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (unsigned*)(ws + w.off_ticket), (int*)ws,
                           num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
-                          w.tiles, k_scale, v_scale};
+                          w.tile_rows, w.tiles, k_scale, v_scale};
+    const bool tc = w.tile_rows > 16;
     const dim3 grid((unsigned)(((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits + kWarps - 1) / kWarps));
-    cudaError_t e = w.nt == 1 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32 * kWarps), 0, st, p)
-                              : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32 * kWarps), 0, st, p);
-    if (e == cudaSuccess && w.max_splits > kTicketSplits)
+    cudaError_t e = tc                  ? launch_attn_kv4_tc(p, w.sms, st)
+                    : w.tile_rows == 8 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32 * kWarps), 0, st, p)
+                                       : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32 * kWarps), 0, st, p);
+    if (e == cudaSuccess && w.max_splits > (tc ? 1 : kTicketSplits))
         e = launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((int64_t)n_seq * stride * n_heads)),
-                       dim3((w.max_splits + 31) / 32 * 32), 0, st, p, 8 * w.nt);
+                       dim3((w.max_splits + 31) / 32 * 32), 0, st, p);
     return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;
 }
 
