@@ -520,7 +520,7 @@ wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_k
 /* wedlm_attention_bf16 over a 4-bit cache: the same q, S, n, out and rules
  * (rows r < n[b] see positions 0 .. S[b] + r; their own K/V must have been
  * appended; rows r >= n[b] are not written; stride <= 1024), with pointers
- * 16-byte aligned and the workspace 256-byte aligned, from
+ * 16-byte aligned, out 32-byte and the workspace 256-byte aligned, from
  * wedlm_attention_kv4_workspace_bytes.  The workspace's first int32 is the
  * device error word.  Zero the whole workspace once: calls leave its counters as
  * they found them and only ever set the error word (1: a page id outside

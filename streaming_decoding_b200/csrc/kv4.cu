@@ -2,6 +2,7 @@
 //
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -630,9 +631,10 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     // half the capacity, and not so short that starting an item shows.
     const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
     const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)(tc ? kItemsPerSmTc : kItemsPerSm) * sms;
-    const int64_t unit = 64, least = tc ? 256 : 64, most = tc ? 2048 : 1024;
+    const int64_t unit = tc ? 128 : 64, least = tc ? 256 : 64, most = tc ? 2048 : 1024;
     int64_t chunk = std::max(least, std::min(most, ((keys + items - 1) / items + unit - 1) / unit * unit));
     chunk = std::max(chunk, ((int64_t)max_ctx + unit * kMaxSplits - 1) / (unit * kMaxSplits) * unit);
+    if (getenv("KV4_CHUNK")) chunk = atoi(getenv("KV4_CHUNK"));  // XXX experiment
     w->chunk = (int)std::min<int64_t>(chunk, 1 << 30);
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
@@ -728,7 +730,7 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
         return WEDLM_ERR_INVALID_ARG;
     if (!power_of_two(k_scale) || !power_of_two(v_scale)) return WEDLM_ERR_INVALID_ARG;
     if (workspace_bytes < (int64_t)w.bytes || ((uintptr_t)workspace & 255)) return WEDLM_ERR_INVALID_ARG;
-    if (((uintptr_t)q | (uintptr_t)kv4_pool | (uintptr_t)out) & 15) return WEDLM_ERR_INVALID_ARG;
+    if ((((uintptr_t)q | (uintptr_t)kv4_pool) & 15) || ((uintptr_t)out & 31)) return WEDLM_ERR_INVALID_ARG;
     if (((uintptr_t)page_table | (uintptr_t)S | (uintptr_t)n) & 3) return WEDLM_ERR_INVALID_ARG;
     char* ws = static_cast<char*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;

@@ -112,7 +112,7 @@ __device__ __forceinline__ void load_page(void* dst, const uint8_t* src, uint64_
 // and worker w of W takes items w, w + W, ...  A tile's place in the numbering
 // comes from prefix sums over the (sequence, tile) groups, which a CTA builds
 // once in shared memory; with more than kGroupCap groups they are walked.
-constexpr int kGroupCap = 512;
+constexpr int kGroupCap = 256;
 
 struct Item {
     int b, h, sp, q0, S, rows, ks, ke, nsplit;

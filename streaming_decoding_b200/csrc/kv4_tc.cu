@@ -1,29 +1,34 @@
 // Attention over the 4-bit cache for sequences with more than 16 query rows to
-// a KV head (windows of several rows, prompts), on tcgen05: a tile of 128 * NT
-// query rows, and of every 64-key block one widened copy of K and V in shared
-// memory that all of the tile's rows share.
+// a KV head (windows of several rows, prompts), on tcgen05: of every 128-key
+// block one widened copy of K and V in shared memory, fp16, and two products
+//   S_t = Q_t K^T   M = 128 rows, N = 128 keys, K = 128 dims  (A = Q_t, B = K: shared memory)
+//   O_t += P_t V    M = 128 rows, N = 128 dims, K = 128 keys  (A = P_t in TMEM over S_t, B = V)
+// for the CTA's two tiles t.  ROWS: the tiles are the two halves of 256 query
+// rows and every block serves both.  Otherwise (at most 128 query rows) the
+// tiles hold the same rows and take the blocks in turn, each with its own
+// maximum, sum and O, joined at the item's end; with at most 64 rows tile 1's
+// rows are repeated on lanes 64 .. 127 and only those are worked on, so that the
+// two tiles' softmax runs on different schedulers.  Operands are fp16: a code
+// times its scale is exact in it, Q is scaled per row by a power of two and P is
+// relative to a lazily raised maximum, as in kv4.cu.
 //
-//   S_t = Q_t K^T   M = 128 rows, N = 64 keys, K = 128 dims  (A = Q_t in TMEM, B = K)
-//   O_t += P_t V    M = 128 rows, N = 128 dims, K = 64 keys  (A = P_t in TMEM, B = V)
-// Operands are fp16: a code times its scale is exact in it, Q is scaled per row
-// by a power of two and P is relative to a lazily raised maximum, as in kv4.cu.
-// Q in TMEM rather than in shared memory: with N = 64 an A operand from shared
-// memory would ask for more than its bandwidth beside the widening's traffic.
+// Why these shapes (measured, cycles): an MMA of N = 32 or 64 takes 45 whatever
+// its A operand, of N = 128 65, the full rate; a commit is seen by a waiting
+// thread after 220, so few and large steps.  Two tiles, because one's softmax
+// (at least 1024 cycles of the exp2 unit a block) then runs under the other's
+// products (1040).  A block and tile pair costs the tensor pipe 2080 cycles
+// (ROWS), the shared memory's bandwidth about 2300.
 //
-// Persistent CTAs (NT = 1: two to an SM, 256 TMEM columns each; NT = 2: one, 512
-// columns), one tile's softmax running while the other tile's (or CTA's)
-// products do.  Warps:
-//   4 NT  softmax: thread i of tile t owns query row 128 t + i (a TMEM lane):
-//         writes Q, turns S into P in place, rescales O when its maximum grows
-//         by more than 2^8, and at an item's end reads O out,
-//   4     widen: warp w takes page w of every block from the ring of raw pages
-//         to the fp16 K and V blocks (128-byte swizzle; V dims contiguous,
-//         used as an MN-major operand),
-//   1     a thread issues the MMAs (and the warp allocates TMEM),
-//   1     bulk copies of the raw pages.
-// Bounds at a 32-row window of 7 heads a KV head: matrix pipe 1024 cycles a
-// 64-key block and tile pair, exp2 unit the same, widening and softmax issue
-// slots about 850.  All waits are bounded; a timeout sets the device error word.
+// Persistent, one CTA to an SM.  Warps:
+//   8  softmax: thread i of tile t owns query row i (a TMEM lane): Q to shared
+//      memory, S to P in place, O rescaled when its maximum grows by more than
+//      2^8, O read out at an item's end,
+//   4  widen: warp w takes pages w and w + 4 of every block from the ring of raw
+//      pages to the fp16 blocks (128-byte swizzle; V dims contiguous, used as an
+//      MN-major operand),
+//   1  a thread issues the MMAs (and the warp allocates TMEM),
+//   1  bulk copies of the raw pages.
+// All waits are bounded; a timeout sets the device error word.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -33,36 +38,35 @@ namespace {
 
 using namespace kv4;
 
-constexpr int KBLK = 64;                      // keys of a block
+constexpr int KBLK = 128;                     // keys of a block
 constexpr int PPB = KBLK / kPage;             // pages of a block
-constexpr int RAW_BYTES = PPB * kHeadPage;    // a block's raw pages
-constexpr int HALF_BYTES = KBLK * 128;        // 64 keys x 64 dims of fp16
-constexpr int BLK_BYTES = 2 * HALF_BYTES;     // a widened K or V block
-constexpr int FLAGS = 16;                     // ring of per-block flags (more than any run-ahead)
-
-template <int NT>
-struct Cfg {
-    static constexpr int CTAS_PER_SM = NT == 1 ? 2 : 1;
-    static constexpr int NRAW = NT == 1 ? 3 : 6;  // raw blocks in flight
-    static constexpr int NKV = NT == 1 ? 2 : 3;   // widened K and V blocks
-    static constexpr int WARP_WIDEN = 4 * NT, WARP_MMA = WARP_WIDEN + 4, WARP_LOAD = WARP_MMA + 1;
-    static constexpr int THREADS = 32 * (WARP_LOAD + 1);
-    static constexpr uint32_t TM_COLS = NT == 1 ? 256 : 512;
-    static constexpr uint32_t tm_s(int t) { return t * 64; }
-    static constexpr uint32_t tm_q(int t) { return NT * 64 + t * 64; }
-    static constexpr uint32_t tm_o(int t) { return NT * 128 + t * 128; }
-    static constexpr int OFF_K = 0;
-    static constexpr int OFF_V = OFF_K + NKV * BLK_BYTES;
-    static constexpr int OFF_RAW = OFF_V + NKV * BLK_BYTES;
-    static constexpr int OFF_ITEMS = OFF_RAW + NRAW * RAW_BYTES;
-    static constexpr int OFF_BAR = OFF_ITEMS + (int)sizeof(ItemTable);
-    static constexpr int NBARS = 2 * NRAW + 4 * NKV + 4 * NT + 1;
-    static constexpr int OFF_FLAGS = OFF_BAR + NBARS * 8;
-    static constexpr int SMEM = OFF_FLAGS + FLAGS * 4 + 16 + 1024 /* alignment */;
-    static_assert(CTAS_PER_SM * (SMEM + 1024) <= 228 * 1024, "shared memory");
-    static_assert(NRAW + NKV + 2 < FLAGS, "flag ring");
-    static_assert(TM_COLS >= (uint32_t)(NT * 256), "TMEM");
-};
+constexpr int RPP = 4;                        // pages of a raw stage (half a block)
+constexpr int RAW_BYTES = RPP * kHeadPage;
+constexpr int HALF_BYTES = KBLK * 128;        // 128 keys (or rows) x 64 dims of fp16
+constexpr int BUF_BYTES = 2 * HALF_BYTES;     // a widened K or V block, or a tile's Q
+constexpr int NRAW = 3;                       // raw stages
+constexpr int NBUF = 4;                       // widened K, V, K, V blocks
+constexpr int FLAGS = 8;                      // ring of per-block flags (more than any run-ahead)
+constexpr int NITEM = 4;                      // ring of items
+constexpr int WARP_WIDEN = 8, WARP_MMA = 12, WARP_LOAD = 13;
+constexpr int THREADS = 16 * 32;               // (two warps idle: register shares go by groups of four)
+// Registers a thread: launched with 128, then shared out by what the roles need.
+constexpr int REGS_SOFTMAX = 152, REGS_WIDEN = 96, REGS_REST = 112;
+static_assert(8 * REGS_SOFTMAX + 4 * REGS_WIDEN + 4 * REGS_REST <= 16 * 128, "more registers than the block was launched with");
+constexpr uint32_t TM_COLS = 512;             // S_t at 128 t, O_t at 256 + 128 t
+constexpr int OFF_BUF = 0;
+constexpr int OFF_Q = OFF_BUF + NBUF * BUF_BYTES;  // ROWS: a Q per tile; else one Q and the exchange of the tiles' O
+constexpr int OFF_RAW = OFF_Q + 2 * BUF_BYTES;
+constexpr int OFF_ITEMS = OFF_RAW + NRAW * RAW_BYTES;
+constexpr int OFF_ML = OFF_ITEMS + (int)sizeof(ItemTable);  // (m, l) of tile 1's rows
+constexpr int OFF_BAR = OFF_ML + 128 * 8;
+constexpr int NBARS = 2 * NRAW + 2 * NBUF + 2 * NITEM + 8 + 1;
+constexpr int OFF_FLAGS = OFF_BAR + NBARS * 8;
+constexpr int OFF_RING = OFF_FLAGS + FLAGS * 4;
+constexpr int SMEM = OFF_RING + NITEM * (int)sizeof(Item) + 16 + 1024 /* alignment */;
+static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(NRAW / 2 + 4 < FLAGS, "flag ring");
+static_assert(sizeof(ItemTable) % 8 == 0, "alignment of what follows");
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -92,6 +96,12 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t addr) {
 // fp16 operands, fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -125,37 +135,107 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+// 32 bytes a thread: a thread writes whole sectors of its own row.
+__device__ __forceinline__ void st_global8(void* p, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+// Waits for the loads issued so far; r: registers that one of them fills (tied, so
+// that no use of them moves ahead of the wait).
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+          "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+          "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+          "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]) : : "memory");
+    asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two fp32 operations in one instruction: (a, b) = (x, y) * s + z and (a, b) += (x, y).
+__device__ __forceinline__ void fma2(float& a, float& b, uint32_t x, uint32_t y, float s, float z) {
+    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmov.b64 w, {%5, %5};\n\t"
+        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+        : "=f"(a), "=f"(b) : "r"(x), "r"(y), "f"(s), "f"(z));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
+        "mov.b64 {%0, %1}, u;\n\t}" : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // The whole warp waits; false for all of it if a lane gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, err));
 }
 
-template <int NT>
-__global__ void __launch_bounds__(Cfg<NT>::THREADS, Cfg<NT>::CTAS_PER_SM) attn_kv4_tc_kernel(const AttnKv4Params p) {
-    using C = Cfg<NT>;
-    constexpr int NRAW = C::NRAW, NKV = C::NKV;
+// 32 dims from c on of a row's O: the output (times f), or the chunk's partial.
+__device__ __forceinline__ void store_row(const AttnKv4Params& p, int nsplit, int sp, int64_t at, int c, uint32_t (&r)[32],
+                                          float f) {
+    if (nsplit == 1) {
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(r[2 * y]) * f, __uint_as_float(r[2 * y + 1]) * f);
+            r[y] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        st_global8(p.out + at * HD + c, r);
+        st_global8(p.out + at * HD + c + 16, r + 8);
+    } else {
+        float* dst = p.part_o + (at * p.max_splits + sp) * HD + c;
+#pragma unroll
+        for (int y = 0; y < 32; y += 8) st_global8(dst + y, r + y);
+    }
+}
+
+// Barrier among the 256 softmax threads, returning whether `v` holds in all of
+// them: steps that synchronise the tiles are entered by all or by none, also
+// when a bounded wait gave up in one warp only.
+__device__ __forceinline__ bool softmax_all(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.and.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)v) : "memory");
+    return r != 0;
+}
+
+template <bool ROWS>
+__global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sK = smem + C::OFF_K;
-    uint8_t* sV = smem + C::OFF_V;
-    uint8_t* raw = smem + C::OFF_RAW;
-    ItemTable& items = *reinterpret_cast<ItemTable*>(smem + C::OFF_ITEMS);
-    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [NRAW] a block's pages are there
-    uint64_t* raw_empty = raw_full + NRAW;                                // [NRAW] widened (4 warps)
-    uint64_t* k_full = raw_empty + NRAW;                                  // [NKV] K block widened (4 warps)
-    uint64_t* k_empty = k_full + NKV;                                     // [NKV] its products done
-    uint64_t* v_full = k_empty + NKV;
-    uint64_t* v_empty = v_full + NKV;
-    uint64_t* q_full = v_empty + NKV;  // [NT] an item's Q is in TMEM (4 warps)
-    uint64_t* s_full = q_full + NT;    // [NT] S of a block done
-    uint64_t* p_full = s_full + NT;    // [NT] P written (4 warps)
-    uint64_t* pv_done = p_full + NT;   // [NT] P V of a block done: S / P free, O settled
-    uint64_t* drain = pv_done + NT;
-    volatile int* flags = reinterpret_cast<volatile int*>(smem + C::OFF_FLAGS);  // bit x: page x of the block is not there
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAGS + FLAGS * 4);
+    uint8_t* bufs = smem + OFF_BUF;
+    uint8_t* sQ = smem + OFF_Q;
+    float* xch = reinterpret_cast<float*>(smem + OFF_Q + BUF_BYTES);  // !ROWS: 64 dims x 128 rows
+    uint8_t* raw = smem + OFF_RAW;
+    ItemTable& items = *reinterpret_cast<ItemTable*>(smem + OFF_ITEMS);
+    float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // [NRAW] a block's pages are there
+    uint64_t* raw_empty = raw_full + NRAW;                             // [NRAW] widened (4 warps)
+    uint64_t* buf_full = raw_empty + NRAW;                             // [NBUF] K or V widened (4 warps)
+    uint64_t* buf_empty = buf_full + NBUF;                             // [NBUF] its products done (by each tile it serves)
+    uint64_t* q_full = buf_empty + NBUF;                               // [2] an item's Q is there (4 warps)
+    uint64_t* s_full = q_full + 2;                                     // [2] S of a tile's block done
+    uint64_t* p_full = s_full + 2;                                     // [2] P written (4 warps)
+    uint64_t* pv_done = p_full + 2;                                    // [2] P V done: S / P free, O settled
+    uint64_t* item_full = pv_done + 2;                                 // [NITEM] an item is in the ring
+    uint64_t* item_empty = item_full + NITEM;                          // [NITEM] every role is past it
+    uint64_t* drain = item_empty + NITEM;
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + OFF_FLAGS);  // bit x: page x of the block is not there
+    // The CTA's items in order, an item with ke <= ks ending them
+    volatile Item* ring = reinterpret_cast<volatile Item*>(smem + OFF_RING);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_RING + NITEM * sizeof(Item));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -163,25 +243,27 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, Cfg<NT>::CTAS_PER_SM) attn_k
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], 4);
         }
-        for (int s = 0; s < NKV; ++s) {
-            mbar_init(&k_full[s], 4);
-            mbar_init(&k_empty[s], 1);
-            mbar_init(&v_full[s], 4);
-            mbar_init(&v_empty[s], 1);
+        for (int s = 0; s < NBUF; ++s) {
+            mbar_init(&buf_full[s], 4);
+            mbar_init(&buf_empty[s], ROWS ? 2 : 1);
         }
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 4);
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&pv_done[t], 1);
         }
+        for (int s = 0; s < NITEM; ++s) {
+            mbar_init(&item_full[s], 1);
+            mbar_init(&item_empty[s], 8 + 4 + 1);  // softmax and widening warps, the MMA thread
+        }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == C::WARP_MMA) {
+    if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(C::TM_COLS) : "memory");
+                     "r"(TM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     griddep_wait();
@@ -193,315 +275,439 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, Cfg<NT>::CTAS_PER_SM) attn_k
     const uint32_t tmem = *tmem_slot;
     int* err = p.err;
     const int g = p.hq / p.hkv;
-    const int workers = gridDim.x;
-    ItemIter it;
-    it.next = blockIdx.x;
-    Item item;
+    auto blocks_of = [](const volatile Item& o) { return (o.ke - o.ks + KBLK - 1) / KBLK; };
 
-    if (warp == C::WARP_LOAD) {
+    if (warp >= WARP_MMA) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_REST));
+    if (warp == WARP_LOAD) {
         // ----------------------------------------------------------- loader
-        // Lane l holds the ids of pages l, l + 32, ... of the item, 32 at a time.
-        uint32_t gb = 0;
+        // Lane l holds the ids of pages l, l + 32, ... of the item, 32 at a time;
+        // lanes 0 .. 7 load the pages of a block.
+        uint32_t gb = 0, gr = 0;
         bool ok = true;
-        while (ok && item_next(it, p, items, workers, item)) {
+        ItemIter it;
+        it.next = blockIdx.x;
+        Item item;
+        for (uint32_t li = 0; ok; ++li) {
+            const bool has = item_next(it, p, items, gridDim.x, item);
+            if (!(ok = warp_wait(&item_empty[li % NITEM], ((li / NITEM) & 1) ^ 1, err))) break;
+            if (lane == 0) {
+                if (!has) item.ke = item.ks = 0;
+                volatile Item& o = ring[li % NITEM];
+                o.b = item.b;
+                o.h = item.h;
+                o.sp = item.sp;
+                o.q0 = item.q0;
+                o.S = item.S;
+                o.rows = item.rows;
+                o.ks = item.ks;
+                o.ke = item.ke;
+                o.nsplit = item.nsplit;
+                bar_arrive(&item_full[li % NITEM]);
+            }
+            __syncwarp();
+            if (!has) break;
             const int32_t* table = p.table + (int64_t)item.b * p.pages_per_seq;
             const int page0 = item.ks / kPage, npages = (item.ke + kPage - 1) / kPage - page0;
-            const int nblk = (npages + PPB - 1) / PPB;
+            const int nblk = blocks_of(item);
             int ids = -1;
-            for (int j = 0; j < nblk; ++j, ++gb) {
-                const int k0 = j * PPB;
+            for (int j = 0; j < nblk && ok; ++j, ++gb) {
+                const int k0 = j * PPB, mine = k0 + (lane & (PPB - 1));
                 if ((k0 & 31) == 0) {
                     const int idx = page0 + k0 + lane;
                     ids = k0 + lane < npages && idx < p.pages_per_seq ? __ldcg(table + idx) : -1;
                 }
-                const int page = __shfl_sync(0xffffffffu, ids, (k0 + (lane & (PPB - 1))) & 31);
-                const bool wanted = k0 + (lane & (PPB - 1)) < npages;
-                const bool there = wanted && page >= 0 && page < p.num_pages;
+                const int page = __shfl_sync(0xffffffffu, ids, mine & 31);
+                const bool wanted = mine < npages, there = wanted && page >= 0 && page < p.num_pages;
                 const uint32_t have = __ballot_sync(0xffffffffu, there && lane < PPB);
                 if (wanted && !there) set_error(err, kErrBounds);
-                const int s = gb % NRAW;
-                if (!(ok = warp_wait(&raw_empty[s], ((gb / NRAW) & 1) ^ 1, err))) break;
-                if (lane == 0) {
-                    flags[gb % FLAGS] = (int)(~have & ((1u << PPB) - 1));
-                    bar_expect(&raw_full[s], __popc(have) * kHeadPage);
+                if (lane == 0) flags[gb % FLAGS] = (int)(~have & ((1u << PPB) - 1));
+#pragma unroll
+                for (int x = 0; x < 2; ++x, ++gr) {  // two stages to a block
+                    const int s = gr % NRAW;
+                    if (!(ok = warp_wait(&raw_empty[s], ((gr / NRAW) & 1) ^ 1, err))) break;
+                    const uint32_t part = (have >> (RPP * x)) & ((1u << RPP) - 1);
+                    if (lane == 0) bar_expect(&raw_full[s], __popc(part) * kHeadPage);
+                    __syncwarp();
+                    if (there && lane < PPB && lane / RPP == x)
+                        load_page(raw + s * RAW_BYTES + (lane % RPP) * kHeadPage,
+                                  p.pool + ((int64_t)page * p.hkv + item.h) * kHeadPage, &raw_full[s]);
                 }
-                __syncwarp();
-                if (there && lane < PPB)
-                    load_page(raw + s * RAW_BYTES + lane * kHeadPage,
-                              p.pool + ((int64_t)page * p.hkv + item.h) * kHeadPage, &raw_full[s]);
             }
         }
         // copies still in flight (only after an error) land before the CTA exits
         if (lane == 0)
-            for (uint32_t j = gb > (uint32_t)NRAW ? gb - NRAW : 0u; j < gb; ++j)
+            for (uint32_t j = gr > (uint32_t)NRAW ? gr - NRAW : 0u; j < gr; ++j)
                 mbar_wait_bounded(smem_u32(&raw_full[j % NRAW]), (j / NRAW) & 1, nullptr, 200000000LL);
-    } else if (warp >= C::WARP_WIDEN && warp < C::WARP_MMA) {
-        // ------------------------------------------------------------ widen
-        // Lane: 16-dim block `blk` of tokens 4 i + tok0 of the warp's page.
-        const int w = warp - C::WARP_WIDEN, blk = lane & 7, tok0 = lane >> 3;
-        const int half = (blk >> 2) * HALF_BYTES;
-        // a block's two 16-byte chunks; lanes of the upper dims write theirs in the
-        // other order, so that eight lanes never meet in a bank
-        const int ch0 = (blk & 3) * 2 + (blk >> 2), ch1 = ch0 ^ 1;
-        uint32_t gb = 0;
-        bool ok = true;
-        while (ok && item_next(it, p, items, workers, item)) {
-            const int page0 = item.ks / kPage, npages = (item.ke + kPage - 1) / kPage - page0;
-            const int nblk = (npages + PPB - 1) / PPB;
-            for (int j = 0; j < nblk; ++j, ++gb) {
-                const int s = gb % NRAW, d = gb % NKV;
-                if (!(ok = warp_wait(&raw_full[s], (gb / NRAW) & 1, err))) break;
-                const uint8_t* src = raw + s * RAW_BYTES + w * kHeadPage;
-                const int key0 = item.ks + j * KBLK + w * kPage;
-                // keys behind the last row's, or of a page that is not there, add nothing
-                const int live = (flags[gb % FLAGS] >> w) & 1 ? 0 : item.ke - key0;
-                uint2 code[4];
-                uint32_t scale[4];
-                auto fetch = [&](const uint8_t* half_page) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int tok = 4 * i + tok0;
-                        code[i] = *reinterpret_cast<const uint2*>(half_page + tok * 64 + blk * 8);
-                        scale[i] = half_page[kCodes + tok * 8 + blk];
-                    }
-                };
-                auto widen = [&](uint8_t* dst) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = w * kPage + 4 * i + tok0;
-                        const uint32_t sc = e4m3x2_to_f16x2(scale[i] * 0x101u);
-                        uint32_t f[8];
-                        e2m1x8_to_f16x2(code[i].x, *reinterpret_cast<uint32_t(*)[4]>(&f[0]));
-                        e2m1x8_to_f16x2(code[i].y, *reinterpret_cast<uint32_t(*)[4]>(&f[4]));
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) f[x] = hmul2(f[x], sc);
-                        uint8_t* row = dst + half + r * 128;
-                        const bool up = blk >> 2;
-                        *reinterpret_cast<uint4*>(row + ((ch0 ^ (r & 7)) << 4)) =
-                            make_uint4(up ? f[4] : f[0], up ? f[5] : f[1], up ? f[6] : f[2], up ? f[7] : f[3]);
-                        *reinterpret_cast<uint4*>(row + ((ch1 ^ (r & 7)) << 4)) =
-                            make_uint4(up ? f[0] : f[4], up ? f[1] : f[5], up ? f[2] : f[6], up ? f[3] : f[7]);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                };
-                fetch(src);
-                if (!(ok = warp_wait(&k_empty[d], ((gb / NKV) & 1) ^ 1, err))) break;
-                widen(sK + d * BLK_BYTES);
-                if (lane == 0) bar_arrive(&k_full[d]);
-                fetch(src + kHalfPage);
-                if (live < kPage) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * i + tok0 >= live) scale[i] = 0;
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&raw_empty[s]);
-                if (!(ok = warp_wait(&v_empty[d], ((gb / NKV) & 1) ^ 1, err))) break;
-                widen(sV + d * BLK_BYTES);
-                if (lane == 0) bar_arrive(&v_full[d]);
-            }
-        }
-    } else if (warp == C::WARP_MMA) {
+    } else if (warp == WARP_MMA) {
         // -------------------------------------------------------------- MMA
         if (lane == 0) {
             constexpr uint32_t idS = idesc_f16(128, KBLK);
             constexpr uint32_t idO = idesc_f16(128, HD) | (1u << 16);  // B (V) MN-major
-            uint32_t gb = 0;
-            int li = 0;
+            // The tiles in turn, P V of a block and then S of the tile's next one: while
+            // one tile's products run, the other's softmax does.
+            uint32_t base = 0;       // the CTA's number of the item's first block
+            uint32_t x[2] = {0, 0};  // the tiles' blocks so far
             bool ok = true;
-            while (ok && item_next(it, p, items, workers, item)) {
-                const int nblk = (item.ke - item.ks + KBLK - 1) / KBLK;
-                for (int j = 0; j < nblk && ok; ++j, ++gb) {
-                    const int d = gb % NKV;
-                    const uint32_t kvpar = (gb / NKV) & 1;
-                    if (!(ok = mbar_wait_bounded(smem_u32(&k_full[d]), kvpar, err))) break;
-                    const uint32_t kb = smem_u32(sK + d * BLK_BYTES), vb = smem_u32(sV + d * BLK_BYTES);
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && mbar_wait_bounded(smem_u32(bar), parity, err); };
+            auto issue_s = [&](int t, uint32_t b) {
+                const uint32_t kx = 2 * b;
+                if (!wait(&buf_full[kx % NBUF], (kx / NBUF) & 1)) return;
+                tc_fence_after();
+                const uint32_t qa = smem_u32(sQ + (ROWS ? t : 0) * BUF_BYTES), kb = smem_u32(bufs + (kx % NBUF) * BUF_BYTES);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        ok = ok && (j == 0 ? mbar_wait_bounded(smem_u32(&q_full[t]), li & 1, err)
-                                           : mbar_wait_bounded(smem_u32(&pv_done[t]), (gb - 1) & 1, err));
-                        if (!ok) break;
-                        tc_fence_after();
+                for (int kk = 0; kk < HD / 16; ++kk)
+                    mma_ss(tmem + 128 * t, sdesc(qa + (kk >> 2) * HALF_BYTES + (kk & 3) * 32),
+                           sdesc(kb + (kk >> 2) * HALF_BYTES + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+                umma_commit(&s_full[t]);
+                umma_commit(&buf_empty[kx % NBUF]);
+            };
+            auto issue_pv = [&](int t, uint32_t b, bool first) {
+                const uint32_t vx = 2 * b + 1;
+                if (!wait(&p_full[t], x[t] & 1) || !wait(&buf_full[vx % NBUF], (vx / NBUF) & 1)) return;
+                tc_fence_after();
+                const uint32_t vb = smem_u32(bufs + (vx % NBUF) * BUF_BYTES);
 #pragma unroll
-                        for (int kk = 0; kk < HD / 16; ++kk)
-                            mma_ts(tmem + C::tm_s(t), tmem + C::tm_q(t) + kk * 8,
-                                   sdesc(kb + (kk >> 2) * HALF_BYTES + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
-                        umma_commit(&s_full[t]);
-                    }
-                    if (!ok) break;
-                    umma_commit(&k_empty[d]);
-                    if (!(ok = mbar_wait_bounded(smem_u32(&v_full[d]), kvpar, err))) break;
+                for (int kk = 0; kk < KBLK / 16; ++kk)
+                    mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_mn(vb + kk * 2048),
+                           idO, (!first || kk > 0) ? 1u : 0u);
+                umma_commit(&pv_done[t]);
+                umma_commit(&buf_empty[vx % NBUF]);
+            };
+            for (uint32_t li = 0; ok; ++li) {
+                if (!wait(&item_full[li % NITEM], (li / NITEM) & 1)) break;
+                const int nblk = blocks_of(ring[li % NITEM]);
+                bar_arrive(&item_empty[li % NITEM]);
+                if (nblk <= 0) break;
+                constexpr int STEP = ROWS ? 1 : 2;  // from one block of a tile to its next
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if (!(ok = ok && mbar_wait_bounded(smem_u32(&p_full[t]), gb & 1, err))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < KBLK / 16; ++kk)
-                            mma_ts(tmem + C::tm_o(t), tmem + C::tm_s(t) + kk * 8, sdesc_mn(vb + kk * 2048), idO,
-                                   (j > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit(&pv_done[t]);
-                    }
-                    if (ok) umma_commit(&v_empty[d]);
+                for (int t = 0; t < 2; ++t) {
+                    if (ROWS || t == 0) wait(&q_full[t], li & 1);
+                    const int j = ROWS ? 0 : t;
+                    if (ok && j < nblk) issue_s(t, base + j);
                 }
-                ++li;
+                for (int j0 = 0; ok && j0 < nblk; j0 += STEP) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int j = j0 + (ROWS ? 0 : t);
+                        if (!ok || j >= nblk) continue;
+                        issue_pv(t, base + j, j0 == 0);
+                        if (ok && j + STEP < nblk && wait(&pv_done[t], x[t] & 1)) issue_s(t, base + j + STEP);
+                        ++x[t];
+                    }
+                }
+                base += nblk;
             }
             // every MMA issued has completed before TMEM may be released
             umma_commit(drain);
             mbar_wait_bounded(smem_u32(drain), 0, nullptr, 200000000LL);
         }
-    } else {
-        // ---------------------------------------------------------- softmax
-        const int t = warp >> 2;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + C::tm_s(t), tQ = tmem + lane_base + C::tm_q(t),
-                       tO = tmem + lane_base + C::tm_o(t);
-        const int row = threadIdx.x;  // of the tile
+    }
+    } else if (warp >= WARP_WIDEN) {
+        // ------------------------------------------------------------ widen
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_WIDEN));
+        // Lane: 16-dim block `blk` of tokens 4 i + tok of the warp's pages.  Lanes of
+        // the upper dims take the token beside the others': the swizzle then sends
+        // the eight lanes of a 16-byte store to eight different places.
+        const int w = warp - WARP_WIDEN, blk = lane & 7, tok = (lane >> 3) ^ (blk >> 2);
+        const int ch = 2 * (blk & 3), base_off = (blk >> 2) * HALF_BYTES + tok * 128;
+        // places of the block's two 16-byte chunks, for tokens tok and tok + 4 (mod 8)
+        const int pos[2][2] = {{(ch ^ tok) << 4, ((ch + 1) ^ tok) << 4}, {(ch ^ (tok + 4)) << 4, ((ch + 1) ^ (tok + 4)) << 4}};
         uint32_t gb = 0;
         bool ok = true;
-        while (ok && item_next(it, p, items, workers, item)) {
-            const int qr = item.q0 + row;
-            const bool live = qr < item.rows;
-            const int qc = min(qr, item.rows - 1);
-            const int64_t at = ((int64_t)item.b * p.stride + qc / g) * p.hq + item.h * g + qc % g;
-            // Q of the row to TMEM, scaled by a power of two
-            int ex = 0;
-            {
-                uint32_t w[64];
-                const uint4* q = reinterpret_cast<const uint4*>(p.q + at * HD);
+        for (uint32_t li = 0; ok; ++li) {
+            if (!(ok = warp_wait(&item_full[li % NITEM], (li / NITEM) & 1, err))) break;
+            const int ks = ring[li % NITEM].ks, ke = ring[li % NITEM].ke, nblk = (ke - ks + KBLK - 1) / KBLK;
+            __syncwarp();
+            if (lane == 0) bar_arrive(&item_empty[li % NITEM]);
+            if (nblk <= 0) break;
+            for (int j = 0; j < nblk && ok; ++j, ++gb) {
+                // K and then V of the warp's page in each half of the block
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t x = 2 * gb + kv;
+                    uint8_t* dst = bufs + (x % NBUF) * BUF_BYTES + base_off;
+                    if (!(ok = warp_wait(&buf_empty[x % NBUF], ((x / NBUF) & 1) ^ 1, err))) break;
+#pragma unroll 1
+                    for (int pg = 0; pg < 2; ++pg) {
+                        const uint32_t r = 2 * gb + pg;
+                        if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAW], (r / NRAW) & 1, err))) break;
+                        const int page = w + RPP * pg;
+                        const uint8_t* src = raw + (r % NRAW) * RAW_BYTES + w * kHeadPage + kv * kHalfPage;
+                        uint2 code[4];
+                        uint32_t scale[4];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const uint4 u = live ? __ldcg(q + x) : make_uint4(0, 0, 0, 0);
-                    w[4 * x] = u.x;
-                    w[4 * x + 1] = u.y;
-                    w[4 * x + 2] = u.z;
-                    w[4 * x + 3] = u.w;
+                        for (int i = 0; i < 4; ++i) {
+                            code[i] = *reinterpret_cast<const uint2*>(src + (4 * i + tok) * 64 + blk * 8);
+                            scale[i] = src[kCodes + (4 * i + tok) * 8 + blk];
+                        }
+                        if (kv) {
+                            // V of keys behind the last row's, or of a page that is not there, is zero
+                            const int gone = flags[gb % FLAGS];
+                            const int live = (gone >> page) & 1 ? 0 : ke - (ks + j * KBLK + page * kPage);
+                            if (live < kPage) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (4 * i + tok >= live) scale[i] = 0;
+                            }
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(&raw_empty[r % NRAW]);  // (both halves of the pages have been read)
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t sc = e4m3x2_to_f16x2(scale[i] * 0x101u);
+                            uint32_t lo[4], hi[4];
+                            e2m1x8_to_f16x2(code[i].x, lo);
+                            e2m1x8_to_f16x2(code[i].y, hi);
+                            uint8_t* row = dst + (page * kPage + 4 * i) * 128;
+                            *reinterpret_cast<uint4*>(row + pos[i & 1][0]) =
+                                make_uint4(hmul2(lo[0], sc), hmul2(lo[1], sc), hmul2(lo[2], sc), hmul2(lo[3], sc));
+                            *reinterpret_cast<uint4*>(row + pos[i & 1][1]) =
+                                make_uint4(hmul2(hi[0], sc), hmul2(hi[1], sc), hmul2(hi[2], sc), hmul2(hi[3], sc));
+                        }
+                    }
+                    if (!ok) break;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&buf_full[x % NBUF]);
                 }
-                uint32_t mx = 0;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
+        const int t = warp >> 2;
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + 128 * t, tO = tmem + lane_base + 256 + 128 * t;
+        const int lane_row = threadIdx.x & 127;
+        uint32_t x = 0, base = 0;  // the tile's and the CTA's blocks so far
+        bool ok = true;
+        for (uint32_t li = 0;; ++li) {
+            ok = warp_wait(&item_full[li % NITEM], (li / NITEM) & 1, err);
+            if (!ROWS) ok = softmax_all(ok);  // (and Q and the exchange have been read)
+            if (!ok) break;
+            const volatile Item& item = ring[li % NITEM];
+            const int nblk = blocks_of(item);
+            if (nblk <= 0) break;
+            const int tile_rows = min(item.rows - item.q0, ROWS ? 256 : 128);
+            const bool twice = !ROWS && tile_rows <= 64;  // rows repeated on lanes 64 .. 127
+            const int row = ROWS ? (int)threadIdx.x : twice ? lane_row & 63 : lane_row;
+            // rows this thread works for: with `twice` tile 0 the lower, tile 1 the upper lanes
+            const bool live = row < tile_rows && (!twice || (lane_row >> 6) == t);
+            const bool warp_live = !twice || ((lane_row >> 6) == t);
+            const int qr = item.q0 + min(row, tile_rows - 1);
+            const int64_t at = ((int64_t)item.b * p.stride + qr / g) * p.hq + item.h * g + qr % g;
+            // Q: the row's largest magnitude first, then (by the tile that writes it) the
+            // scaled row, a quarter at a time to spare registers
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + at * HD);
+            uint32_t mx = 0;
 #pragma unroll
-                for (int x = 0; x < 64; ++x) mx = max(mx, max(w[x] & 0x7FFFu, (w[x] >> 16) & 0x7FFFu));
-                ex = mx ? min(100, 14 + 127 - (int)(mx >> 7)) : 0;
+            for (int y = 0; y < 16; ++y) {
+                const uint4 u = row < tile_rows ? __ldcg(q + y) : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+            }
+            const int ex = mx ? min(100, 14 + 127 - (int)(mx >> 7)) : 0;
+            if (ROWS || t == 0) {
                 const float f = __int_as_float((ex + 127) << 23);
+                uint8_t* dst = sQ + (ROWS ? t : 0) * BUF_BYTES + lane_row * 128;
+#pragma unroll 1
+                for (int y0 = 0; y0 < 16; y0 += 4) {
 #pragma unroll
-                for (int x = 0; x < 64; ++x)
-                    w[x] = pack_half2(__uint_as_float(w[x] << 16) * f, __uint_as_float(w[x] & 0xFFFF0000u) * f);
-                tmem_st32(tQ, &w[0]);
-                tmem_st32(tQ + 32, &w[32]);
-                tmem_wait_st();
-                tc_fence_before();
+                    for (int y1 = 0; y1 < 4; ++y1) {
+                        const int y = y0 + y1;
+                        const uint4 u = row < tile_rows ? __ldcg(q + y) : make_uint4(0, 0, 0, 0);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o[k] = pack_half2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+                        *reinterpret_cast<uint4*>(dst + (y >> 3) * HALF_BYTES + (((y & 7) ^ (lane_row & 7)) << 4)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) bar_arrive(&q_full[t]);
             }
             const float sl = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale * __int_as_float((127 - ex) << 23);
-            const int lim = min(item.S + qc / g, item.ke - 1);              // last key the row sees
-            const int all = min(item.S + item.q0 / g, item.ke - 1);         // last key every row of the tile sees
-            const int nblk = (item.ke - item.ks + KBLK - 1) / KBLK;
+            const int lim = min(item.S + qr / g, item.ke - 1);               // last key the row sees
+            const int all = min(item.S + item.q0 / g, item.ke - 1);          // last key every row of the tile sees
+            const int ks = item.ks, nsplit = item.nsplit, sp = item.sp;
+            __syncwarp();
+            if (lane == 0) bar_arrive(&item_empty[li % NITEM]);
             float m = -INFINITY, z = 1e30f, l = 0.f;
-            for (int j = 0; j < nblk; ++j, ++gb) {
-                if (!(ok = warp_wait(&s_full[t], gb & 1, err))) break;
+            bool any = false;  // O holds something
+            for (int j = ROWS ? 0 : t; j < nblk; j += ROWS ? 1 : 2, ++x) {
+                if (!(ok = warp_wait(&s_full[t], x & 1, err))) break;
                 tc_fence_after();
-                const int key0 = item.ks + j * KBLK;
-                float e[64];
-                tmem_ld32(tS, reinterpret_cast<uint32_t*>(&e[0]));
-                tmem_ld32(tS + 32, reinterpret_cast<uint32_t*>(&e[32]));
-                const int gone = flags[gb % FLAGS];
-                tmem_wait_ld();
-                if (key0 + KBLK - 1 > all || gone) {
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (key0 + x > lim || ((gone >> (x / kPage)) & 1)) e[x] = -INFINITY;
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < 64; ++x) top = fmaxf(top, e[x]);
-                const float v = top * sl;
-                const bool grew = fmaf(top, sl, z) > kWeightLog2 + kLazyLog2;
-                if (__any_sync(0xffffffffu, grew)) {
-                    const float f = grew ? exp2_fast(m - v) : 1.f;
-                    if (grew) {
-                        m = v;
-                        z = kWeightLog2 - v;
-                        l *= f;
-                    }
-                    if (j > 0) {
+                if (warp_live) {
+                    const int key0 = ks + j * KBLK;
+                    const int gone = flags[(base + j) % FLAGS];  // (written before the block's K was)
+                    // (Loops are kept rolled: four roles share the instruction cache.)
+                    if (key0 + KBLK - 1 > all || gone) {
+                        // scores of keys that are not visible to -inf, in place
 #pragma unroll 1
-                        for (int x = 0; x < HD; x += 32) {
+                        for (int c = 0; c < KBLK; c += 32) {
                             uint32_t r[32];
-                            tmem_ld32(tO + x, r);
-                            tmem_wait_ld();
+                            tmem_ld32(tS + c, r);
+                            tmem_wait_ld(r);
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) r[y] = __float_as_uint(__uint_as_float(r[y]) * f);
-                            tmem_st32(tO + x, r);
+                            for (int y = 0; y < 32; ++y)
+                                if (key0 + c + y > lim || ((gone >> ((c + y) / kPage)) & 1)) r[y] = 0xFF800000u;
+                            tmem_st32(tS + c, r);
+                        }
+                        tmem_wait_st();
+                    }
+                    uint32_t ra[32], rb[32];  // scores of 32 keys each, one set loaded while the other is used
+                    float mx[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) mx[y] = -INFINITY;
+                    auto take_max = [&](const uint32_t (&r)[32]) {
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2)
+                            mx[(y >> 1) & 3] = max3(mx[(y >> 1) & 3], __uint_as_float(r[y]), __uint_as_float(r[y + 1]));
+                    };
+                    tmem_ld32(tS, ra);
+#pragma unroll 1
+                    for (int c = 0; c < KBLK; c += 64) {
+                        tmem_wait_ld(ra);
+                        tmem_ld32(tS + c + 32, rb);
+                        take_max(ra);
+                        tmem_wait_ld(rb);
+                        tmem_ld32(tS + (c + 64) % KBLK, ra);  // (at last the first ones again, for the weights)
+                        take_max(rb);
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grew = fmaf(top, sl, z) > kWeightLog2 + kLazyLog2;
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float v = top * sl, f = grew ? exp2_fast(m - v) : 1.f;
+                        if (grew) {
+                            m = v;
+                            z = kWeightLog2 - v;
+                            l *= f;
+                        }
+                        if (any) {
+                            // (the tile's last P V was done before this S was issued)
+#pragma unroll 1
+                            for (int c = 0; c < HD; c += 32) {
+                                tmem_ld32(tO + c, rb);
+                                tmem_wait_ld(rb);
+#pragma unroll
+                                for (int y = 0; y < 32; ++y) rb[y] = __float_as_uint(__uint_as_float(rb[y]) * f);
+                                tmem_st32(tO + c, rb);
+                            }
                         }
                     }
-                }
-                uint32_t pk[32];
-                float sum[4] = {};
+                    float sum[4] = {};
+                    // P of 32 keys over the first half of their own S: the arguments, then the
+                    // exponentials, then the sums, so that the exp2 unit is fed without a pause
+                    auto weigh = [&](int c, const uint32_t (&r)[32]) {
+                        uint32_t pk[16];
+                        float v[32];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    const float a = exp2_fast(fmaf(e[2 * x], sl, z)), b = exp2_fast(fmaf(e[2 * x + 1], sl, z));
-                    sum[x & 3] += a + b;
-                    pk[x] = pack_half2(a, b);
+                        for (int y = 0; y < 32; y += 2) fma2(v[y], v[y + 1], r[y], r[y + 1], sl, z);
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) v[y] = exp2_fast(v[y]);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) pk[y / 2] = pack_half2(v[y], v[y + 1]);
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) add2(sum[y & 2], sum[(y & 2) + 1], v[y], v[y + 1]);
+                        tmem_st16(tS + c, pk);
+                    };
+#pragma unroll 1
+                    for (int c = 0; c < KBLK; c += 64) {
+                        tmem_wait_ld(ra);
+                        tmem_ld32(tS + c + 32, rb);
+                        weigh(c, ra);
+                        tmem_wait_ld(rb);
+                        if (c + 64 < KBLK) tmem_ld32(tS + c + 64, ra);
+                        weigh(c + 32, rb);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_wait_st();
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st32(tS, pk);
-                tmem_wait_st();
+                any = true;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bar_arrive(&p_full[t]);
             }
-            if (!ok) break;
-            // O of the item
-            if (!(ok = warp_wait(&pv_done[t], (gb - 1) & 1, err))) break;
-            tc_fence_after();
-            const float f = out_factor(p.v_scale, l);
-#pragma unroll 1
-            for (int x = 0; x < HD; x += 32) {
-                uint32_t r[32];
-                tmem_ld32(tO + x, r);
-                tmem_wait_ld();
-                if (!live) continue;
-                if (item.nsplit == 1) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * HD + x);
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 h2 =
-                                __floats2bfloat162_rn(__uint_as_float(r[8 * y + 2 * k]) * f, __uint_as_float(r[8 * y + 2 * k + 1]) * f);
-                            o[k] = *reinterpret_cast<const uint32_t*>(&h2);
-                        }
-                        dst[y] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.part_o + (at * p.max_splits + item.sp) * HD + x);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) dst[y] = make_uint4(r[4 * y], r[4 * y + 1], r[4 * y + 2], r[4 * y + 3]);
-                }
+            base += nblk;
+            if (ok && any) {
+                ok = warp_wait(&pv_done[t], (x - 1) & 1, err);
+                tc_fence_after();
             }
-            if (live && item.nsplit > 1) p.part_ml[at * p.max_splits + item.sp] = make_float2(m, l);
+            if (ROWS) {
+                if (!ok) break;
+                const float f = out_factor(p.v_scale, l);
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + c, r);
+                    tmem_wait_ld(r);
+                    if (live) store_row(p, nsplit, sp, at, c, r, f);
+                }
+                if (live && nsplit > 1) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
+            } else {
+                // tile 1's result joins tile 0's: O = 2^(m0 - M) O0 + 2^(m1 - M) O1, M = max(m0, m1)
+                if (t == 1 && live) s_ml[row] = make_float2(m, l);
+                if (!(ok = softmax_all(ok))) break;
+                float f = 0.f, f1 = 0.f;
+                if (t == 0 && live) {
+                    const float2 o = s_ml[row];
+                    const float M = fmaxf(m, o.x);
+                    f = m == -INFINITY ? 0.f : exp2_fast(m - M);
+                    f1 = o.x == -INFINITY ? 0.f : exp2_fast(o.x - M);
+                    l = f * l + f1 * o.y;
+                    m = M;
+                }
+                const float inv = out_factor(p.v_scale, l);
+#pragma unroll 1
+                for (int c = 0; c < HD; c += 32) {
+                    uint32_t r[32];
+                    // (warps whose lanes have nothing to do skip the load)
+                    if (any && warp_live) {
+                        tmem_ld32(tO + c, r);
+                        tmem_wait_ld(r);
+                    }
+                    float* x_row = xch + (c & 32) * 128 + row;
+                    if (t == 1 && live) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) x_row[y * 128] = any ? __uint_as_float(r[y]) : 0.f;
+                    }
+                    if (!(ok = softmax_all(ok))) break;
+                    if (t == 0 && live) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float own = f > 0.f ? f * __uint_as_float(r[y]) : 0.f;
+                            r[y] = __float_as_uint(f1 > 0.f ? fmaf(f1, x_row[y * 128], own) : own);
+                        }
+                        store_row(p, nsplit, sp, at, c, r, inv);
+                    }
+                }
+                if (!ok) break;
+                if (t == 0 && live && nsplit > 1) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
+            }
             tc_fence_before();
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == C::WARP_MMA) {
+    if (warp == WARP_MMA) {
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TM_COLS) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TM_COLS) : "memory");
     }
 }
 
-template <int NT>
+template <bool ROWS>
 cudaError_t launch(const AttnKv4Params& p, int num_sms, cudaStream_t st) {
-    using C = Cfg<NT>;
-    // (cheap, and needed once per device)
-    cudaError_t e = cudaFuncSetAttribute(attn_kv4_tc_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(attn_kv4_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     const int64_t most = (int64_t)p.n_seq * p.hkv * p.tiles * p.max_splits;
-    const int grid = (int)std::min<int64_t>(most, (int64_t)C::CTAS_PER_SM * num_sms);
-    return launch_pdl(attn_kv4_tc_kernel<NT>, dim3(grid), dim3(C::THREADS), C::SMEM, st, p);
+    const int grid = (int)std::min<int64_t>(most, num_sms);
+    return launch_pdl(attn_kv4_tc_kernel<ROWS>, dim3(grid), dim3(THREADS), SMEM, st, p);
 }
 
 }  // namespace
@@ -509,7 +715,7 @@ cudaError_t launch(const AttnKv4Params& p, int num_sms, cudaStream_t st) {
 namespace kv4 {
 
 cudaError_t launch_attn_kv4_tc(const AttnKv4Params& p, int num_sms, cudaStream_t st) {
-    return p.tile_rows <= 128 ? launch<1>(p, num_sms, st) : launch<2>(p, num_sms, st);
+    return p.tile_rows <= 128 ? launch<false>(p, num_sms, st) : launch<true>(p, num_sms, st);
 }
 
 }  // namespace kv4
