@@ -2,7 +2,6 @@
 //
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -195,7 +194,6 @@ constexpr int kStep = 2;              // pages taken together
 constexpr int kStepKeys = kStep * kPage;
 constexpr int kStages = 2;
 constexpr int kItemsPerSm = 48;
-constexpr int kItemsPerSmTc = 6;
 constexpr int kTicketSplits = 8;      // up to this many chunks the last one to finish joins them
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -627,14 +625,36 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     w->tiles = (rows + w->tile_rows - 1) / w->tile_rows;
     const bool tc = w->tile_rows > 16;
     // Chunks by the call's capacity alone (a sequence's result does not depend on
-    // its neighbours' lengths): some items for every SM when the sequences are at
-    // half the capacity, and not so short that starting an item shows.
+    // its neighbours' lengths).
     const int64_t pairs = (int64_t)n_seq * hkv * w->tiles;
-    const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)(tc ? kItemsPerSmTc : kItemsPerSm) * sms;
-    const int64_t unit = tc ? 128 : 64, least = tc ? 256 : 64, most = tc ? 2048 : 1024;
-    int64_t chunk = std::max(least, std::min(most, ((keys + items - 1) / items + unit - 1) / unit * unit));
-    chunk = std::max(chunk, ((int64_t)max_ctx + unit * kMaxSplits - 1) / (unit * kMaxSplits) * unit);
-    if (getenv("KV4_CHUNK")) chunk = atoi(getenv("KV4_CHUNK"));  // XXX experiment
+    int64_t chunk;
+    if (tc) {
+        // The number of chunks whose rounds of items (one CTA an SM) cost the least,
+        // averaged over sequences at the capacity and at half of it: an item costs
+        // its 128-key blocks and about two more to start and end, the chunks' joining
+        // about half a block for every 64 MB of partial results.
+        double best = 0.;
+        chunk = 0;
+        for (int s = 1; s <= kMaxSplits; ++s) {
+            const int64_t c = ((int64_t)max_ctx + 128LL * s - 1) / (128LL * s) * 128;
+            double cost = s > 1 ? 2. + (double)pairs * std::min(rows, w->tile_rows) * s * 512. / (128 << 20) : 0.;
+            for (int half = 0; half < 2; ++half) {
+                const int64_t len = std::max(1, half ? max_ctx / 2 : max_ctx);
+                const int64_t items = pairs * ((len + c - 1) / c);
+                cost += (double)((items + sms - 1) / sms) * (double)((std::min(c, len) + 127) / 128 + 2);
+            }
+            if (chunk == 0 || cost < best) {
+                best = cost;
+                chunk = c;
+            }
+            if (c <= 256) break;
+        }
+    } else {
+        // Some items (warps) for every SM when the sequences are at half the capacity, 64 to 1024 keys.
+        const int64_t keys = pairs * std::max(1, max_ctx / 2), items = (int64_t)kItemsPerSm * sms;
+        chunk = std::max<int64_t>(64, std::min<int64_t>(1024, ((keys + items - 1) / items + 63) / 64 * 64));
+        chunk = std::max<int64_t>(chunk, ((int64_t)max_ctx + 64LL * kMaxSplits - 1) / (64LL * kMaxSplits) * 64);
+    }
     w->chunk = (int)std::min<int64_t>(chunk, 1 << 30);
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;

@@ -160,15 +160,27 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Two fp32 operations in one instruction: (a, b) = (x, y) * s + z and (a, b) += (x, y).
-__device__ __forceinline__ void fma2(float& a, float& b, uint32_t x, uint32_t y, float s, float z) {
-    asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %4};\n\tmov.b64 w, {%5, %5};\n\t"
-        "fma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
-        : "=f"(a), "=f"(b) : "r"(x), "r"(y), "f"(s), "f"(z));
+// Two fp32 values as one operand, and two operations in one instruction.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
-__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
-    asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 u, u, v;\n\t"
-        "mov.b64 {%0, %1}, u;\n\t}" : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -600,20 +612,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                             }
                         }
                     }
-                    float sum[4] = {};
+                    uint64_t sum[2] = {0, 0};
+                    const uint64_t sl2 = pair(sl, sl), z2 = pair(z, z);
                     // P of 32 keys over the first half of their own S: the arguments, then the
                     // exponentials, then the sums, so that the exp2 unit is fed without a pause
                     auto weigh = [&](int c, const uint32_t (&r)[32]) {
                         uint32_t pk[16];
-                        float v[32];
+                        float2 v[16];
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) fma2(v[y], v[y + 1], r[y], r[y + 1], sl, z);
+                        for (int y = 0; y < 16; ++y) v[y] = unpair(fma2(pair(r[2 * y], r[2 * y + 1]), sl2, z2));
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) v[y] = exp2_fast(v[y]);
+                        for (int y = 0; y < 16; ++y) v[y] = make_float2(exp2_fast(v[y].x), exp2_fast(v[y].y));
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) pk[y / 2] = pack_half2(v[y], v[y + 1]);
+                        for (int y = 0; y < 16; ++y) pk[y] = pack_half2(v[y].x, v[y].y);
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2) add2(sum[y & 2], sum[(y & 2) + 1], v[y], v[y + 1]);
+                        for (int y = 0; y < 16; ++y) sum[y & 1] = add2(sum[y & 1], pair(v[y].x, v[y].y));
                         tmem_st16(tS + c, pk);
                     };
 #pragma unroll 1
@@ -625,7 +638,8 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         if (c + 64 < KBLK) tmem_ld32(tS + c + 64, ra);
                         weigh(c + 32, rb);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 both = unpair(add2(sum[0], sum[1]));
+                    l += both.x + both.y;
                     tmem_wait_st();
                 }
                 any = true;
