@@ -188,9 +188,26 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// mbar_wait_bounded without its long suspension: these waits are short and on
+// the critical path (a woken thread went on 300 cycles sooner).
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity, int* err) {
+    const uint32_t a = smem_u32(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(a, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (stalled(err)) return false;
+            if (clock64() - t0 > 2000000000LL) {
+                set_error(err, kErrTimeout);
+                return false;
+            }
+        }
+    }
+}
 // The whole warp waits; false for all of it if a lane gave up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(bar), parity, err));
+    return __all_sync(0xffffffffu, wait_short(bar, parity, err));
 }
 
 // 32 dims from c on of a row's O: the output (times f), or the chunk's partial.
@@ -358,31 +375,38 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             constexpr uint32_t idO = idesc_f16(128, HD) | (1u << 16);  // B (V) MN-major
             // The tiles in turn, P V of a block and then S of the tile's next one: while
             // one tile's products run, the other's softmax does.
-            uint32_t base = 0;       // the CTA's number of the item's first block
-            uint32_t x[2] = {0, 0};  // the tiles' blocks so far
+            // (Rolled over the tiles and with descriptors that only add constants: this
+            // thread's code competes with the other roles' for the instruction cache,
+            // and a miss delays every product.)
+            uint32_t base = 0;  // the CTA's number of the item's first block
+            uint32_t xs = 0;    // bit t: parity of the tile's blocks so far
             bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && mbar_wait_bounded(smem_u32(bar), parity, err); };
-            auto issue_s = [&](int t, uint32_t b) {
+            const uint64_t dq = sdesc(smem_u32(sQ)), dk = sdesc(smem_u32(bufs)), dv = sdesc_mn(smem_u32(bufs));
+            constexpr uint64_t BUF16 = BUF_BYTES >> 4, HALF16 = HALF_BYTES >> 4;
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_short(bar, parity, err); };
+            // (A look at a barrier takes over a hundred cycles beside the widening's
+            // stores, so the widened block is waited for before what it waits for anyway.)
+            auto issue_s = [&](int t, uint32_t b, uint64_t* after, uint32_t after_parity) {
                 const uint32_t kx = 2 * b;
-                if (!wait(&buf_full[kx % NBUF], (kx / NBUF) & 1)) return;
+                if (!wait(&buf_full[kx % NBUF], (kx / NBUF) & 1) || !wait(after, after_parity)) return;
                 tc_fence_after();
-                const uint32_t qa = smem_u32(sQ + (ROWS ? t : 0) * BUF_BYTES), kb = smem_u32(bufs + (kx % NBUF) * BUF_BYTES);
+                const uint64_t q = dq + (ROWS ? t : 0) * BUF16, k = dk + (kx % NBUF) * BUF16;
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk)
-                    mma_ss(tmem + 128 * t, sdesc(qa + (kk >> 2) * HALF_BYTES + (kk & 3) * 32),
-                           sdesc(kb + (kk >> 2) * HALF_BYTES + (kk & 3) * 32), idS, kk > 0 ? 1u : 0u);
+                    mma_ss(tmem + 128 * t, q + (kk >> 2) * HALF16 + (kk & 3) * 2, k + (kk >> 2) * HALF16 + (kk & 3) * 2, idS,
+                           kk > 0 ? 1u : 0u);
                 umma_commit(&s_full[t]);
                 umma_commit(&buf_empty[kx % NBUF]);
             };
             auto issue_pv = [&](int t, uint32_t b, bool first) {
                 const uint32_t vx = 2 * b + 1;
-                if (!wait(&p_full[t], x[t] & 1) || !wait(&buf_full[vx % NBUF], (vx / NBUF) & 1)) return;
+                if (!wait(&buf_full[vx % NBUF], (vx / NBUF) & 1) || !wait(&p_full[t], (xs >> t) & 1)) return;
                 tc_fence_after();
-                const uint32_t vb = smem_u32(bufs + (vx % NBUF) * BUF_BYTES);
+                const uint64_t v = dv + (vx % NBUF) * BUF16;
 #pragma unroll
                 for (int kk = 0; kk < KBLK / 16; ++kk)
-                    mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_mn(vb + kk * 2048),
-                           idO, (!first || kk > 0) ? 1u : 0u);
+                    mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + (kk >> 1) * 32 + (kk & 1) * 8, v + kk * 128, idO,
+                           (!first || kk > 0) ? 1u : 0u);
                 umma_commit(&pv_done[t]);
                 umma_commit(&buf_empty[vx % NBUF]);
             };
@@ -392,20 +416,21 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                 bar_arrive(&item_empty[li % NITEM]);
                 if (nblk <= 0) break;
                 constexpr int STEP = ROWS ? 1 : 2;  // from one block of a tile to its next
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (ROWS || t == 0) wait(&q_full[t], li & 1);
-                    const int j = ROWS ? 0 : t;
-                    if (ok && j < nblk) issue_s(t, base + j);
-                }
-                for (int j0 = 0; ok && j0 < nblk; j0 += STEP) {
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
+                // The tiles in turn: P V of a block (from the tile's second turn on), then S
+                // of its next one.
+#pragma unroll 1
+                for (int j0 = -STEP; ok && j0 < nblk; j0 += STEP) {
+#pragma unroll 1
+                    for (int t = 0; t < 2 && ok; ++t) {
                         const int j = j0 + (ROWS ? 0 : t);
-                        if (!ok || j >= nblk) continue;
-                        issue_pv(t, base + j, j0 == 0);
-                        if (ok && j + STEP < nblk && wait(&pv_done[t], x[t] & 1)) issue_s(t, base + j + STEP);
-                        ++x[t];
+                        if (j0 < 0) {
+                            if (j + STEP < nblk) issue_s(t, base + j + STEP, &q_full[ROWS ? t : 0], li & 1);
+                            else if (!ROWS) wait(&q_full[0], li & 1);  // (every phase is looked at)
+                        } else if (j < nblk) {
+                            issue_pv(t, base + j, j0 == 0);
+                            if (ok && j + STEP < nblk) issue_s(t, base + j + STEP, &pv_done[t], (xs >> t) & 1);
+                            xs ^= 1u << t;
+                        }
                     }
                 }
                 base += nblk;
