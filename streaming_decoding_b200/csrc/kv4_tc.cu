@@ -23,9 +23,9 @@
 //   8  softmax: thread i of tile t owns query row i (a TMEM lane): Q to shared
 //      memory, S to P in place, O rescaled when its maximum grows by more than
 //      2^8, O read out at an item's end,
-//   4  widen: warp w takes pages w and w + 4 of every block from the ring of raw
-//      pages to the fp16 blocks (128-byte swizzle; V dims contiguous, used as an
-//      MN-major operand),
+//   8  widen: warp w takes page w of every block from the ring of raw pages to
+//      the fp16 blocks (128-byte swizzle; V dims contiguous, used as an MN-major
+//      operand),
 //   1  a thread issues the MMAs (and the warp allocates TMEM),
 //   1  bulk copies of the raw pages.
 // All waits are bounded; a timeout sets the device error word.
@@ -48,18 +48,19 @@ constexpr int NRAW = 3;                       // raw stages
 constexpr int NBUF = 4;                       // widened K, V, K, V blocks
 constexpr int FLAGS = 8;                      // ring of per-block flags (more than any run-ahead)
 constexpr int NITEM = 4;                      // ring of items
-constexpr int WARP_WIDEN = 8, WARP_MMA = 12, WARP_LOAD = 13;
-constexpr int THREADS = 16 * 32;               // (two warps idle: register shares go by groups of four)
-// Registers a thread: launched with 128, then shared out by what the roles need.
-constexpr int REGS_SOFTMAX = 152, REGS_WIDEN = 96, REGS_REST = 112;
-static_assert(8 * REGS_SOFTMAX + 4 * REGS_WIDEN + 4 * REGS_REST <= 16 * 128, "more registers than the block was launched with");
+constexpr int WARP_WIDEN = 8, WARP_MMA = 16, WARP_LOAD = 17;
+constexpr int THREADS = 20 * 32;               // (two warps idle: register shares go by groups of four)
+// Registers a thread: launched with 96, then shared out by what the roles need.
+constexpr int REGS_SOFTMAX = 144, REGS_WIDEN = 56, REGS_REST = 80;
+static_assert(8 * REGS_SOFTMAX + 8 * REGS_WIDEN + 4 * REGS_REST <= 20 * 96, "more registers than the block was launched with");
 constexpr uint32_t TM_COLS = 512;             // S_t at 128 t, O_t at 256 + 128 t
 constexpr int OFF_BUF = 0;
 constexpr int OFF_Q = OFF_BUF + NBUF * BUF_BYTES;  // ROWS: a Q per tile; else one Q and the exchange of the tiles' O
 constexpr int OFF_RAW = OFF_Q + 2 * BUF_BYTES;
 constexpr int OFF_ITEMS = OFF_RAW + NRAW * RAW_BYTES;
 constexpr int OFF_ML = OFF_ITEMS + (int)sizeof(ItemTable);  // (m, l) of tile 1's rows
-constexpr int OFF_BAR = OFF_ML + 128 * 8;
+constexpr int OFF_EX = OFF_ML + 128 * 8;                    // !ROWS: the exponents added to Q's rows
+constexpr int OFF_BAR = OFF_EX + 128 * 4;
 constexpr int NBARS = 2 * NRAW + 2 * NBUF + 2 * NITEM + 8 + 1;
 constexpr int OFF_FLAGS = OFF_BAR + NBARS * 8;
 constexpr int OFF_RING = OFF_FLAGS + FLAGS * 4;
@@ -250,9 +251,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
     uint8_t* raw = smem + OFF_RAW;
     ItemTable& items = *reinterpret_cast<ItemTable*>(smem + OFF_ITEMS);
     float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
+    int* s_ex = reinterpret_cast<int*>(smem + OFF_EX);
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // [NRAW] a block's pages are there
-    uint64_t* raw_empty = raw_full + NRAW;                             // [NRAW] widened (4 warps)
-    uint64_t* buf_full = raw_empty + NRAW;                             // [NBUF] K or V widened (4 warps)
+    uint64_t* raw_empty = raw_full + NRAW;                             // [NRAW] read (a warp a page)
+    uint64_t* buf_full = raw_empty + NRAW;                             // [NBUF] K or V widened (8 warps)
     uint64_t* buf_empty = buf_full + NBUF;                             // [NBUF] its products done (by each tile it serves)
     uint64_t* q_full = buf_empty + NBUF;                               // [2] an item's Q is there (4 warps)
     uint64_t* s_full = q_full + 2;                                     // [2] S of a tile's block done
@@ -270,10 +272,10 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
     if (threadIdx.x == 0) {
         for (int s = 0; s < NRAW; ++s) {
             mbar_init(&raw_full[s], 1);
-            mbar_init(&raw_empty[s], 4);
+            mbar_init(&raw_empty[s], RPP);
         }
         for (int s = 0; s < NBUF; ++s) {
-            mbar_init(&buf_full[s], 4);
+            mbar_init(&buf_full[s], PPB);
             mbar_init(&buf_empty[s], ROWS ? 2 : 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
         }
         for (int s = 0; s < NITEM; ++s) {
             mbar_init(&item_full[s], 1);
-            mbar_init(&item_empty[s], 8 + 4 + 1);  // softmax and widening warps, the MMA thread
+            mbar_init(&item_empty[s], 8 + PPB + 1);  // softmax and widening warps, the MMA thread
         }
         mbar_init(drain, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
     } else if (warp >= WARP_WIDEN) {
         // ------------------------------------------------------------ widen
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_WIDEN));
-        // Lane: 16-dim block `blk` of tokens 4 i + tok of the warp's pages.  Lanes of
+        // Lane: 16-dim block `blk` of tokens 4 i + tok of the warp's page.  Lanes of
         // the upper dims take the token beside the others': the swizzle then sends
         // the eight lanes of a 16-byte store to eight different places.
         const int w = warp - WARP_WIDEN, blk = lane & 7, tok = (lane >> 3) ^ (blk >> 2);
@@ -459,51 +461,46 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             if (lane == 0) bar_arrive(&item_empty[li % NITEM]);
             if (nblk <= 0) break;
             for (int j = 0; j < nblk && ok; ++j, ++gb) {
-                // K and then V of the warp's page in each half of the block
+                // K and then V of the warp's page
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t x = 2 * gb + kv;
                     uint8_t* dst = bufs + (x % NBUF) * BUF_BYTES + base_off;
                     if (!(ok = warp_wait(&buf_empty[x % NBUF], ((x / NBUF) & 1) ^ 1, err))) break;
-#pragma unroll 1
-                    for (int pg = 0; pg < 2; ++pg) {
-                        const uint32_t r = 2 * gb + pg;
-                        if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAW], (r / NRAW) & 1, err))) break;
-                        const int page = w + RPP * pg;
-                        const uint8_t* src = raw + (r % NRAW) * RAW_BYTES + w * kHeadPage + kv * kHalfPage;
-                        uint2 code[4];
-                        uint32_t scale[4];
+                    const uint32_t r = 2 * gb + w / RPP;
+                    if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAW], (r / NRAW) & 1, err))) break;
+                    const uint8_t* src = raw + (r % NRAW) * RAW_BYTES + (w % RPP) * kHeadPage + kv * kHalfPage;
+                    uint2 code[4];
+                    uint32_t scale[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            code[i] = *reinterpret_cast<const uint2*>(src + (4 * i + tok) * 64 + blk * 8);
-                            scale[i] = src[kCodes + (4 * i + tok) * 8 + blk];
-                        }
-                        if (kv) {
-                            // V of keys behind the last row's, or of a page that is not there, is zero
-                            const int gone = flags[gb % FLAGS];
-                            const int live = (gone >> page) & 1 ? 0 : ke - (ks + j * KBLK + page * kPage);
-                            if (live < kPage) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    if (4 * i + tok >= live) scale[i] = 0;
-                            }
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(&raw_empty[r % NRAW]);  // (both halves of the pages have been read)
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t sc = e4m3x2_to_f16x2(scale[i] * 0x101u);
-                            uint32_t lo[4], hi[4];
-                            e2m1x8_to_f16x2(code[i].x, lo);
-                            e2m1x8_to_f16x2(code[i].y, hi);
-                            uint8_t* row = dst + (page * kPage + 4 * i) * 128;
-                            *reinterpret_cast<uint4*>(row + pos[i & 1][0]) =
-                                make_uint4(hmul2(lo[0], sc), hmul2(lo[1], sc), hmul2(lo[2], sc), hmul2(lo[3], sc));
-                            *reinterpret_cast<uint4*>(row + pos[i & 1][1]) =
-                                make_uint4(hmul2(hi[0], sc), hmul2(hi[1], sc), hmul2(hi[2], sc), hmul2(hi[3], sc));
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        code[i] = *reinterpret_cast<const uint2*>(src + (4 * i + tok) * 64 + blk * 8);
+                        scale[i] = src[kCodes + (4 * i + tok) * 8 + blk];
                     }
-                    if (!ok) break;
+                    if (kv) {
+                        // V of keys behind the last row's, or of a page that is not there, is zero
+                        const int gone = flags[gb % FLAGS];
+                        const int live = (gone >> w) & 1 ? 0 : ke - (ks + j * KBLK + w * kPage);
+                        if (live < kPage) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (4 * i + tok >= live) scale[i] = 0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&raw_empty[r % NRAW]);  // (K and V of the page have been read)
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t sc = e4m3x2_to_f16x2(scale[i] * 0x101u);
+                        uint32_t lo[4], hi[4];
+                        e2m1x8_to_f16x2(code[i].x, lo);
+                        e2m1x8_to_f16x2(code[i].y, hi);
+                        uint8_t* row = dst + (w * kPage + 4 * i) * 128;
+                        *reinterpret_cast<uint4*>(row + pos[i & 1][0]) =
+                            make_uint4(hmul2(lo[0], sc), hmul2(lo[1], sc), hmul2(lo[2], sc), hmul2(lo[3], sc));
+                        *reinterpret_cast<uint4*>(row + pos[i & 1][1]) =
+                            make_uint4(hmul2(hi[0], sc), hmul2(hi[1], sc), hmul2(hi[2], sc), hmul2(hi[3], sc));
+                    }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) bar_arrive(&buf_full[x % NBUF]);
@@ -534,39 +531,48 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             const bool warp_live = !twice || ((lane_row >> 6) == t);
             const int qr = item.q0 + min(row, tile_rows - 1);
             const int64_t at = ((int64_t)item.b * p.stride + qr / g) * p.hq + item.h * g + qr % g;
-            // Q: the row's largest magnitude first, then (by the tile that writes it) the
-            // scaled row, a quarter at a time to spare registers
-            const uint4* q = reinterpret_cast<const uint4*>(p.q + at * HD);
-            uint32_t mx = 0;
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-                const uint4 u = row < tile_rows ? __ldcg(q + y) : make_uint4(0, 0, 0, 0);
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-            }
-            const int ex = mx ? min(100, 14 + 127 - (int)(mx >> 7)) : 0;
+            // Q by the tile that owns it: each thread brings its row to the row's place in
+            // shared memory, finds its largest magnitude and scales it there.  (Rolled:
+            // at a kernel's start every instruction comes from far away.)
+            int ex;
             if (ROWS || t == 0) {
-                const float f = __int_as_float((ex + 127) << 23);
                 uint8_t* dst = sQ + (ROWS ? t : 0) * BUF_BYTES + lane_row * 128;
-#pragma unroll 1
-                for (int y0 = 0; y0 < 16; y0 += 4) {
-#pragma unroll
-                    for (int y1 = 0; y1 < 4; ++y1) {
-                        const int y = y0 + y1;
-                        const uint4 u = row < tile_rows ? __ldcg(q + y) : make_uint4(0, 0, 0, 0);
-                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[k] = pack_half2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-                        *reinterpret_cast<uint4*>(dst + (y >> 3) * HALF_BYTES + (((y & 7) ^ (lane_row & 7)) << 4)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(p.q + at * HD);
+                const uint32_t bytes = row < tile_rows ? 16 : 0;  // 0: zeros
+#pragma unroll 4
+                for (int y = 0; y < 16; ++y)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                                 ::"r"(smem_u32(dst + (y >> 3) * HALF_BYTES + (((y & 7) ^ (lane_row & 7)) << 4))),
+                                 "l"(src + 16 * y), "r"(bytes) : "memory");
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                // (chunks in an order that keeps eight threads in different banks)
+                auto chunk = [&](int y) {
+                    return reinterpret_cast<uint4*>(dst + (y >> 3) * HALF_BYTES + (((y & 7) ^ (lane_row & 7)) << 4));
+                };
+                uint32_t mx = 0;
+#pragma unroll 4
+                for (int y = 0; y < 16; ++y) {
+                    const uint4 u = *chunk(y);
+                    mx = max(mx, max(max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu)));
+                    mx = max(mx, max(max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu), max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu)));
                 }
+                ex = mx ? min(100, 14 + 127 - (int)(mx >> 7)) : 0;
+                const float f = __int_as_float((ex + 127) << 23);
+                auto scaled = [&](uint32_t w) {
+                    return pack_half2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                };
+#pragma unroll 2
+                for (int y = 0; y < 16; ++y) {
+                    const uint4 u = *chunk(y);
+                    *chunk(y) = make_uint4(scaled(u.x), scaled(u.y), scaled(u.z), scaled(u.w));
+                }
+                if (!ROWS) s_ex[lane_row] = ex;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) bar_arrive(&q_full[t]);
+            } else {
+                ok = warp_wait(&q_full[0], li & 1, err);
+                ex = s_ex[lane_row];
             }
             const float sl = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale * __int_as_float((127 - ex) << 23);
             const int lim = min(item.S + qr / g, item.ke - 1);               // last key the row sees
