@@ -2,7 +2,6 @@
 //
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -189,12 +188,10 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(T* k, T* v, RowsParams p)
 // to a running maximum that is only raised when a score exceeds it by 2^8, and
 // times 2^6, so weights down to 2^-30 of the largest are kept; sums and
 // outputs are fp32.
-constexpr int kWarps = 4;              // items (warps) of a CTA
 constexpr int kStep = 2;              // pages taken together
-constexpr int kStepKeys = kStep * kPage;
 constexpr int kStages = 2;
 constexpr int kItemsPerSm = 48;
-constexpr int kTicketSplits = 8;      // up to this many chunks the last one to finish joins them
+constexpr int kTicketSplits = 8;      // up to this many chunks the last one to finish joins them (8 lanes a row)
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -276,23 +273,20 @@ __device__ __forceinline__ void join_range(const AttnKv4Params& p, int64_t at, i
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(const AttnKv4Params p) {
+__global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const AttnKv4Params p) {
     constexpr int kRows = 8 * NT;
-    __shared__ __align__(128) uint8_t rings[kWarps][kStages][kStep][kHeadPage];
-    __shared__ __align__(8) uint64_t all_bars[kWarps][kStages];
+    __shared__ __align__(128) uint8_t ring[kStages][kStep][kHeadPage];
+    __shared__ __align__(8) uint64_t bars[kStages];
     griddep_wait();
     griddep_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, j8 = lane >> 2;
-    auto& ring = rings[warp];
-    uint64_t* bars = all_bars[warp];
+    const int lane = threadIdx.x, c = lane & 3, j8 = lane >> 2;
     const int g = p.hq / p.hkv;
-    int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+    int64_t id = blockIdx.x;
     const int tile = (int)(id % p.tiles);
     id /= p.tiles;
     const int sp = (int)(id % p.max_splits);
     id /= p.max_splits;
     const int h = (int)(id % p.hkv), b = (int)(id / p.hkv);
-    if (b >= p.n_seq) return;
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
     const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
     const int ks = sp * p.chunk, page0 = ks / kPage;
@@ -380,15 +374,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
         m[t][0] = m[t][1] = -INFINITY;
         z[t][0] = z[t][1] = 1e30f;
     }
-    // kStep pages from key0 on; `edge`: some of the keys are not visible to some row,
-    // or (bits of `out`) a page is not there.
-    auto step = [&](const uint8_t* base_page, int key0, uint32_t out, auto edge_) {
-        constexpr bool edge = decltype(edge_)::value;
-        // S^T: lane's rows are keys j8 and j8 + 8 of each page
-        float sc[kStep][NT][4] = {};
-#pragma unroll
-        for (int pg = 0; pg < kStep; ++pg) {
-            const uint8_t* K = base_page + pg * kHeadPage;
+    // A page's 16 keys.  (One body, its masks under a branch: the loop stays small
+    // enough for the instruction cache.)
+    auto step = [&](const uint8_t* K, int key0) {
+        const uint8_t* V = K + kHalfPage;
+        const bool edge = key0 + kPage - 1 > lim_min;
+        // S^T: lane's rows are keys j8 and j8 + 8
+        float sc[NT][4] = {}, sd[NT][4] = {};  // (two sums, so that half as many products wait for one another)
+        {
             const uint4 u0 = *reinterpret_cast<const uint4*>(K + j8 * 64 + c * 16);
             const uint4 u1 = *reinterpret_cast<const uint4*>(K + j8 * 64 + 512 + c * 16);
             const uint32_t s0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(K + kCodes + j8 * 8 + c * 2));
@@ -407,32 +400,51 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
                     const uint32_t a2 = hmul2(a[2 * y + 1], f0[x >> 1]), a3 = hmul2(d[2 * y + 1], f1[x >> 1]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
-                        mma_f16(sc[pg][t], a0, a1, a2, a3, qf[t][4 * x + 2 * y], qf[t][4 * x + 2 * y + 1]);
+                        mma_f16(y ? sd[t] : sc[t], a0, a1, a2, a3, qf[t][4 * x + 2 * y], qf[t][4 * x + 2 * y + 1]);
                 }
             }
-        }
-        float top = -INFINITY;
-        float e[kStep][NT][4];
-#pragma unroll
-        for (int pg = 0; pg < kStep; ++pg)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (edge && (key0 + pg * kPage + j8 + 8 * (x >> 1) > lim[t][x & 1] || ((out >> pg) & 1)))
-                        sc[pg][t][x] = -INFINITY;
-                    e[pg][t][x] = fmaf(sc[pg][t][x], sl[t][x & 1], z[t][x & 1]);
-                    top = fmaxf(top, e[pg][t][x]);
-                }
+                for (int x = 0; x < 4; ++x) sc[t][x] += sd[t][x];
+        }
+        // V^T: lane's rows are dims 16 j8 .. + 15, its columns keys 2c, 2c + 1, 8 + 2c, 9 + 2c
+        uint2 u[4];
+        uint32_t vs[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int tok = t * 8 + 2 * c;
+            u[2 * t] = *reinterpret_cast<const uint2*>(V + tok * 64 + j8 * 8);
+            u[2 * t + 1] = *reinterpret_cast<const uint2*>(V + tok * 64 + 64 + j8 * 8);
+            vs[2 * t] = V[kCodes + tok * 8 + j8];
+            vs[2 * t + 1] = V[kCodes + tok * 8 + 8 + j8];
+        }
+        if (edge) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    if (key0 + j8 + 8 * (x >> 1) > lim[t][x & 1]) sc[t][x] = -INFINITY;
+            // V of keys past the last row's: whatever their bytes say, they add nothing
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (key0 + 8 * (x >> 1) + 2 * c + (x & 1) >= ke) vs[x] = 0;
+        }
+        float top = -INFINITY;
+        float e[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                e[t][x] = fmaf(sc[t][x], sl[t][x & 1], z[t][x & 1]);
+                top = fmaxf(top, e[t][x]);
+            }
         if (__any_sync(0xffffffffu, top > kWeightLog2 + kLazyLog2)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float v = -INFINITY;
-#pragma unroll
-                    for (int pg = 0; pg < kStep; ++pg)
-                        v = fmaxf(v, fmaxf(sc[pg][t][x] * sl[t][x], sc[pg][t][2 + x] * sl[t][x]));
+                    float v = fmaxf(sc[t][x] * sl[t][x], sc[t][2 + x] * sl[t][x]);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
                     if (v > m[t][x]) {
@@ -441,64 +453,43 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
                         z[t][x] = kWeightLog2 - v;
                         l[t][x] *= f;
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            o[u][t][x] *= f;
-                            o[u][t][2 + x] *= f;
+                        for (int y = 0; y < 8; ++y) {
+                            o[y][t][x] *= f;
+                            o[y][t][2 + x] *= f;
                         }
                     }
-#pragma unroll
-                    for (int pg = 0; pg < kStep; ++pg) {
-                        e[pg][t][x] = fmaf(sc[pg][t][x], sl[t][x], z[t][x]);
-                        e[pg][t][2 + x] = fmaf(sc[pg][t][2 + x], sl[t][x], z[t][x]);
-                    }
+                    e[t][x] = fmaf(sc[t][x], sl[t][x], z[t][x]);
+                    e[t][2 + x] = fmaf(sc[t][2 + x], sl[t][x], z[t][x]);
                 }
         }
+        uint32_t bt[NT][2];
 #pragma unroll
-        for (int pg = 0; pg < kStep; ++pg) {
-            uint32_t bt[NT][2];
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    e[pg][t][x] = exp2_fast(e[pg][t][x]);
-                    l[t][x & 1] += e[pg][t][x];
-                }
-                bt[t][0] = transpose8x8(pack_half2(e[pg][t][0], e[pg][t][1]));
-                bt[t][1] = transpose8x8(pack_half2(e[pg][t][2], e[pg][t][3]));
+            for (int x = 0; x < 4; ++x) {
+                e[t][x] = exp2_fast(e[t][x]);
+                l[t][x & 1] += e[t][x];
             }
-            // V^T: lane's rows are dims 16 j8 .. + 15, its columns keys 2c, 2c + 1, 8 + 2c, 9 + 2c
-            const uint8_t* V = base_page + pg * kHeadPage + kHalfPage;
-            uint2 u[4];
-            uint32_t s2[2];
+            bt[t][0] = transpose8x8(pack_half2(e[t][0], e[t][1]));
+            bt[t][1] = transpose8x8(pack_half2(e[t][2], e[t][3]));
+        }
+        const uint32_t s2[2] = {e4m3x2_to_f16x2(vs[0] | vs[1] << 8), e4m3x2_to_f16x2(vs[2] | vs[3] << 8)};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            // bytes of (key, key + 1) codes: even dims, then odd dims, of 8 dims
+            uint32_t ev[2][4], od[2][4];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const int tok = t * 8 + 2 * c;
-                u[2 * t] = *reinterpret_cast<const uint2*>(V + tok * 64 + j8 * 8);
-                u[2 * t + 1] = *reinterpret_cast<const uint2*>(V + tok * 64 + 64 + j8 * 8);
-                uint32_t b0 = V[kCodes + tok * 8 + j8], b1 = V[kCodes + tok * 8 + 8 + j8];
-                if (edge) {  // keys past the last row's: whatever their bytes say, they add nothing
-                    if (key0 + pg * kPage + tok >= ke || ((out >> pg) & 1)) b0 = 0;
-                    if (key0 + pg * kPage + tok + 1 >= ke || ((out >> pg) & 1)) b1 = 0;
-                }
-                s2[t] = e4m3x2_to_f16x2(b0 | b1 << 8);
+                const uint32_t w0 = x ? u[2 * t].y : u[2 * t].x, w1 = x ? u[2 * t + 1].y : u[2 * t + 1].x;
+                e2m1x8_to_f16x2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), ev[t]);
+                e2m1x8_to_f16x2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), od[t]);
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                // bytes of (key, key + 1) codes: even dims, then odd dims, of 8 dims
-                uint32_t ev[2][4], od[2][4];
+            for (int y = 0; y < 4; ++y) {
+                const uint32_t a0 = hmul2(ev[0][y], s2[0]), a1 = hmul2(od[0][y], s2[0]);
+                const uint32_t a2 = hmul2(ev[1][y], s2[1]), a3 = hmul2(od[1][y], s2[1]);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint32_t w0 = x ? u[2 * t].y : u[2 * t].x, w1 = x ? u[2 * t + 1].y : u[2 * t + 1].x;
-                    e2m1x8_to_f16x2((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), ev[t]);
-                    e2m1x8_to_f16x2(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), od[t]);
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t a0 = hmul2(ev[0][y], s2[0]), a1 = hmul2(od[0][y], s2[0]);
-                    const uint32_t a2 = hmul2(ev[1][y], s2[1]), a3 = hmul2(od[1][y], s2[1]);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_f16(o[4 * x + y][t], a0, a1, a2, a3, bt[t][0], bt[t][1]);
-                }
+                for (int t = 0; t < NT; ++t) mma_f16(o[4 * x + y][t], a0, a1, a2, a3, bt[t][0], bt[t][1]);
             }
         }
     };
@@ -507,9 +498,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
         const int key0 = (page0 + k * kStep) * kPage;
         ok = mbar_wait_bounded(smem_u32(&bars[s]), par, p.err) && ok;
         __syncwarp();
-        const uint32_t out = (gone >> (kStep * s)) & ((1u << kStep) - 1);
-        if (key0 + kStepKeys - 1 > lim_min || out) step(ring[s][0], key0, out, std::true_type());
-        else step(ring[s][0], key0, 0, std::false_type());
+#pragma unroll 1
+        for (int pg = 0; pg < kStep; ++pg)
+            if (!((gone >> (kStep * s + pg)) & 1)) step(ring[s][pg], key0 + pg * kPage);
         __syncwarp();  // every lane has read the stage
         if (issued < steps) issue();
         if (++s == kStages) {
@@ -555,12 +546,38 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 2) attn_kv4_kernel(
         last = atomicInc(p.tickets + ((int64_t)b * p.hkv + h) * p.tiles + tile, nsplit - 1) == (unsigned)nsplit - 1;
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
-    for (int r = q0; r < min(q0 + kRows, rows); ++r) {
+    // Eight lanes a row, four rows at a time: lane x of the eight holds chunk x's
+    // (m, l) and 16 of the dims.
+    const int x8 = lane & 7, end = min(q0 + kRows, rows);
+    for (int r0 = q0; r0 < end; r0 += 4) {
+        const int r = min(r0 + (lane >> 3), end - 1);
         const int64_t at = (row0 + r / g) * p.hq + h * g + r % g;
-        float mm, ll;
-        float4 acc;
-        join_range(p, at, 0, nsplit, lane, mm, ll, acc);
-        store_out(p, at, lane, acc, out_factor(p.v_scale, ll));
+        const float2 ml = x8 < nsplit ? __ldcg(p.part_ml + at * p.max_splits + x8) : make_float2(-INFINITY, 0.f);
+        const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + x8;
+        float mm = ml.x;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        const float w = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - mm);
+        float ll = w * ml.y;
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+        float4 acc[4] = {};
+#pragma unroll 2
+        for (int s = 0; s < nsplit; ++s) {
+            const float f = __shfl_sync(0xffffffffu, w, (lane & 24) + s);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float4 v = __ldcg(po + s * (HD / 4) + 8 * d);
+                acc[d].x += f * v.x;
+                acc[d].y += f * v.y;
+                acc[d].z += f * v.z;
+                acc[d].w += f * v.w;
+            }
+        }
+        if (r0 + (lane >> 3) < end) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) store_out(p, at, x8 + 8 * d, acc[d], out_factor(p.v_scale, ll));
+        }
     }
 }
 
@@ -759,10 +776,10 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
                           num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
                           w.tile_rows, w.tiles, k_scale, v_scale};
     const bool tc = w.tile_rows > 16;
-    const dim3 grid((unsigned)(((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits + kWarps - 1) / kWarps));
+    const dim3 grid((unsigned)((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits));
     cudaError_t e = tc                  ? launch_attn_kv4_tc(p, w.sms, st)
-                    : w.tile_rows == 8 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32 * kWarps), 0, st, p)
-                                       : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32 * kWarps), 0, st, p);
+                    : w.tile_rows == 8 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32), 0, st, p)
+                                       : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32), 0, st, p);
     if (e == cudaSuccess && w.max_splits > (tc ? 1 : kTicketSplits))
         e = launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((int64_t)n_seq * stride * n_heads)),
                        dim3((w.max_splits + 31) / 32 * 32), 0, st, p);
