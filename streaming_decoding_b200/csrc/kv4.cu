@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(T* k, T* v, Ro
 
 // Four blocks of a lane (more loads in flight, one look-up for all) where a launch
 // has rows enough to fill the GPU with that, else one (more warps).  In and back
-// out, 8 heads: 16 x 1024 bf16 rows 38 us with four, 60 with one (168 MB at 6.5 TB/s:
+// out, 8 heads: 16 x 1024 bf16 rows 38 us with four, 60 with one (158 MB at 6.5 TB/s:
 // 24 us; bound by the instructions of the conversions and by the latency of the
 // look-up); 16 x 16 fp32 rows 5.4 us with one, 8.6 with four (latency alone).
 template <typename T>
