@@ -14,6 +14,13 @@
 // The kernels wait for the kernel before them before they read anything and
 // never let the kernel after them start early: kernels of the decode step read
 // page tables, lengths and cached keys before their own dependency wait.
+//
+// A plan is a chain of dependent reads, each a trip to L2 (some 0.7 us) whatever
+// its size: its lists lie in shared memory where they fit, the first reference
+// counts are read at the start, and what needs no decision (the table rows of a
+// fork) is left to the copy.  Freeing 64 branches, forking 8 sequences eightfold
+// (28 layers, 57 MB copied) and reserving for them: 30.6 us in a graph, with every
+// list in global memory 47; three branches of a small cache: 12.4, and 17.4.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -22,12 +29,13 @@ namespace wedlm {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanShared = 2048;  // entries of a list that a plan keeps in shared memory
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 4;  // 16-byte vectors per thread in flight
 
 // Workspace: [0] the error word, [1] the number of planned copies, then the
 // copies (source, destination), one int per page (free pages, marks or the
-// map of a compaction) and two ints per sequence (marks, offsets).
+// map of a compaction) and three ints per sequence (marks, offsets, a value).
 struct PagesWs {
     int* err;
     int* count;
@@ -35,13 +43,14 @@ struct PagesWs {
     int* list;
     int* mark;
     int* off;
+    int* val;
 };
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t pages_ws_bytes(int32_t num_pages, int32_t n_seq) {
     return 256 + round256((size_t)num_pages * sizeof(int2)) + round256((size_t)num_pages * 4) +
-           2 * round256((size_t)n_seq * 4);
+           3 * round256((size_t)n_seq * 4);
 }
 
 PagesWs pages_ws(void* ws, int32_t num_pages, int32_t n_seq) {
@@ -57,6 +66,8 @@ PagesWs pages_ws(void* ws, int32_t num_pages, int32_t n_seq) {
     w.mark = reinterpret_cast<int*>(c);
     c += round256((size_t)n_seq * 4);
     w.off = reinterpret_cast<int*>(c);
+    c += round256((size_t)n_seq * 4);
+    w.val = reinterpret_cast<int*>(c);
     return w;
 }
 
@@ -100,12 +111,12 @@ __device__ __forceinline__ void load_refs(const int32_t* refs, int64_t i, int nu
 
 // The `want` lowest pages without a reference, ascending, into list[]; returns
 // how many there are (at most want).  Stops scanning once it has them.
-__device__ int find_free(const int32_t* refs, int num_pages, int want, int* list) {
+// `r` holds the thread's counts of the first 4 kPlanThreads pages.
+__device__ int find_free(const int32_t* refs, int num_pages, int want, int* list, int (&r)[4]) {
     int have = 0;
     for (int64_t i0 = 0; i0 < num_pages && have < want; i0 += 4 * kPlanThreads) {
         const int64_t i = i0 + 4 * threadIdx.x;
-        int r[4];
-        load_refs(refs, i, num_pages, 1, r);
+        if (i0 > 0) load_refs(refs, i, num_pages, 1, r);
         int c = 0, total;
 #pragma unroll
         for (int k = 0; k < 4; ++k) c += r[k] == 0;
@@ -167,29 +178,44 @@ __global__ void __launch_bounds__(kPlanThreads) pages_copy_plan_kernel(const int
     if (threadIdx.x == 0) *w.count = cnt;
 }
 
+// Lists of a plan with n entries over n_seq sequences: two values an entry, what
+// it asks for, marks of the sequences.
+struct PlanLists {
+    int val[2][kPlanShared], off[kPlanShared], mark[kPlanShared];
+};
+
 __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const int32_t* seqs, const int32_t* tokens, int n,
                                                                      wedlm_kv_pages p, PagesWs w) {
     griddep_wait();
+    extern __shared__ __align__(16) char smem[];
+    PlanLists& t = *reinterpret_cast<PlanLists*>(smem);
+    const bool small = p.n_seq <= kPlanShared;  // (n <= n_seq)
+    int* mark = small ? t.mark : w.mark;
+    int* off = small ? t.off : w.off;
+    int* held_by = small ? t.val[0] : w.val;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int refs[4];
+    load_refs(p.refs, 4 * threadIdx.x, p.num_pages, 1, refs);
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int q = __ldcg(seqs + i);
-        if (q >= 0 && q < p.n_seq) w.mark[q] = 0;
+        if (q >= 0 && q < p.n_seq) mark[q] = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int q = __ldcg(seqs + i);
-        if (q >= 0 && q < p.n_seq) atomicAdd(&w.mark[q], 1);
+        if (q >= 0 && q < p.n_seq) atomicAdd(&mark[q], 1);
     }
     __syncthreads();
     // The pages each entry asks for.
     for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int q = __ldcg(seqs + i), t = __ldcg(tokens + i);
-        bool ok = q >= 0 && q < p.n_seq && t >= 0 && (int64_t)t <= (int64_t)p.pages_per_seq * kPage;
-        if (ok) ok = __ldcg(&w.mark[q]) == 1;
-        int need = 0;
+        const int q = __ldcg(seqs + i), tok = __ldcg(tokens + i);
+        bool ok = q >= 0 && q < p.n_seq && tok >= 0 && (int64_t)tok <= (int64_t)p.pages_per_seq * kPage;
+        if (ok) ok = mark[q] == 1;
+        int need = 0, held = 0;
         if (ok) {
             const int32_t* row = p.page_table + (int64_t)q * p.pages_per_seq;
-            int held = 0, first = p.pages_per_seq;
+            int first = p.pages_per_seq;
+#pragma unroll 4
             for (int j = lane; j < p.pages_per_seq; j += 32) {
                 if (__ldcg(row + j) >= 0) ++held;
                 else first = min(first, j);
@@ -197,125 +223,136 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const int32
             held = __reduce_add_sync(0xffffffffu, held);
             first = __reduce_min_sync(0xffffffffu, first);
             ok = held == first;  // no place empty before one that is taken
-            need = max(0, (t + kPage - 1) / kPage - held);
+            need = max(0, (tok + kPage - 1) / kPage - held);
         }
         if (lane == 0) {
             if (!ok) set_error(w.err, kErrBounds);
-            w.off[i] = ok ? need : 0;
+            off[i] = ok ? need : 0;
+            held_by[i] = held;
         }
     }
     __syncthreads();
-    const int total = scan_needs(w.off, n);
-    const int have = find_free(p.refs, p.num_pages, total, w.list);
+    const int total = scan_needs(off, n);
+    int* list = total <= kPlanShared ? t.val[1] : w.list;
+    const int have = find_free(p.refs, p.num_pages, total, list, refs);
     __syncthreads();
     if (have < total) {
         if (threadIdx.x == 0) set_error(w.err, kErrPages);
         return;
     }
     for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int at = w.off[i], need = (i + 1 < n ? w.off[i + 1] : total) - at;
+        const int at = off[i], need = (i + 1 < n ? off[i + 1] : total) - at;
         if (need == 0) continue;
-        int32_t* row = p.page_table + (int64_t)__ldcg(seqs + i) * p.pages_per_seq;
-        int held = 0;
-        for (int j = lane; j < p.pages_per_seq; j += 32) held += __ldcg(row + j) >= 0;
-        held = __reduce_add_sync(0xffffffffu, held);
+        int32_t* row = p.page_table + (int64_t)__ldcg(seqs + i) * p.pages_per_seq + held_by[i];
         for (int j = lane; j < need; j += 32) {
-            const int page = w.list[at + j];
-            row[held + j] = page;
+            const int page = list[at + j];
+            row[j] = page;
             p.refs[page] = 1;
         }
     }
     __threadfence();
 }
 
+// Leaves in w.val[i] the full pages that child i is to share with its parent,
+// or -1 for an entry that is not served: the copy kernel fills those in.
 __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const int32_t* parents, const int32_t* children,
                                                                        int n, wedlm_kv_pages p, PagesWs w) {
     griddep_wait();
+    extern __shared__ __align__(16) char smem[];
+    PlanLists& t = *reinterpret_cast<PlanLists*>(smem);
+    const bool small = p.n_seq <= kPlanShared;  // (n <= n_seq)
+    int* mark = small ? t.mark : w.mark;
+    int* off = small ? t.off : w.off;
+    int* len = small ? t.val[0] : w.val;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int refs[4];
+    load_refs(p.refs, 4 * threadIdx.x, p.num_pages, 1, refs);
     auto in = [&](int q) { return q >= 0 && q < p.n_seq; };
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int a = __ldcg(parents + i), c = __ldcg(children + i);
-        if (in(a)) w.mark[a] = 0;
-        if (in(c)) w.mark[c] = 0;
+        if (in(a)) mark[a] = 0;
+        if (in(c)) mark[c] = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlanThreads) {
         const int a = __ldcg(parents + i), c = __ldcg(children + i);
-        if (in(a)) atomicOr(&w.mark[a], 1 << 30);
-        if (in(c)) atomicAdd(&w.mark[c], 1);
+        len[i] = in(a) ? __ldcg(p.S + a) : -1;
+        if (in(a)) atomicOr(&mark[a], 1 << 30);
+        if (in(c)) atomicAdd(&mark[c], 1);
     }
     __syncthreads();
-    // off[i]: 1 when entry i needs a page of its own, for the parent's last page
-    // that is not full; -1 for an entry that cannot be served.
+    // len[i]: the tokens entry i shares, -1 when it cannot be served; off[i]: 1 when
+    // it needs a page of its own, for the parent's last page that is not full.
     for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int a = __ldcg(parents + i), c = __ldcg(children + i);
-        bool ok = in(a) && in(c);
-        int L = 0;
-        if (ok) {
-            L = __ldcg(p.S + a);
-            ok = __ldcg(&w.mark[c]) == 1 && L >= 0 && (int64_t)L <= (int64_t)p.pages_per_seq * kPage;
-        }
+        const int a = __ldcg(parents + i), c = __ldcg(children + i), L = len[i];
+        bool ok = in(a) && in(c) && L >= 0 && (int64_t)L <= (int64_t)p.pages_per_seq * kPage;
+        if (ok) ok = mark[c] == 1;
         if (ok) {
             const int32_t* row = p.page_table + (int64_t)a * p.pages_per_seq;
-            for (int j = lane; j < (L + kPage - 1) / kPage; j += 32) {
-                const int page = __ldcg(row + j);
-                if (page < 0 || page >= p.num_pages || __ldcg(p.refs + page) <= 0) ok = false;
-            }
             const int32_t* own = p.page_table + (int64_t)c * p.pages_per_seq;
-            for (int j = lane; j < p.pages_per_seq; j += 32) ok = ok && __ldcg(own + j) < 0;
+            const int pages = (L + kPage - 1) / kPage;
+            for (int j0 = lane; j0 < p.pages_per_seq; j0 += 128) {
+                int page[4], count[4], mine[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = j0 + 32 * k;
+                    page[k] = j < pages ? __ldcg(row + j) : 0;
+                    mine[k] = j < p.pages_per_seq ? __ldcg(own + j) : -1;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    ok = ok && page[k] >= 0 && page[k] < p.num_pages && mine[k] < 0;
+                    count[k] = ok && j0 + 32 * k < pages ? __ldcg(p.refs + page[k]) : 1;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ok = ok && count[k] > 0;
+            }
         }
         ok = __all_sync(0xffffffffu, ok);
         if (lane == 0) {
-            if (!ok) set_error(w.err, kErrBounds);
-            if (in(c)) w.mark[c] = ok ? 1 : 2;  // 2: this entry's child is left alone
-            w.off[i] = ok ? (L % kPage != 0) : 0;
-        }
-    }
-    __syncthreads();
-    const int total = scan_needs(w.off, n);
-    const int have = find_free(p.refs, p.num_pages, total, w.list);
-    __syncthreads();
-    if (threadIdx.x == 0) *w.count = have < total ? 0 : total;
-    if (have < total) {
-        if (threadIdx.x == 0) set_error(w.err, kErrPages);
-        return;
-    }
-    for (int i = warp; i < n; i += kPlanThreads / 32) {
-        const int a = __ldcg(parents + i), c = __ldcg(children + i);
-        if (!in(a) || !in(c) || __ldcg(&w.mark[c]) != 1) continue;
-        const int32_t* from = p.page_table + (int64_t)a * p.pages_per_seq;
-        int32_t* to = p.page_table + (int64_t)c * p.pages_per_seq;
-        const int L = __ldcg(p.S + a), full = L / kPage;
-        for (int j = lane; j < full; j += 32) {
-            const int page = __ldcg(from + j);
-            to[j] = page;
-            atomicAdd(p.refs + page, 1);
-        }
-        if (lane == 0) {
-            p.S[c] = L;
-            if (L % kPage) {
-                const int at = w.off[i], page = w.list[at];
-                to[full] = page;
-                p.refs[page] = 1;
-                w.pairs[at] = make_int2(__ldcg(from + full), page);
+            if (!ok) {
+                set_error(w.err, kErrBounds);
+                len[i] = -1;
             }
+            off[i] = ok ? (L % kPage != 0) : 0;
+        }
+    }
+    __syncthreads();
+    const int total = scan_needs(off, n);
+    int* list = total <= kPlanShared ? t.val[1] : w.list;
+    const int have = find_free(p.refs, p.num_pages, total, list, refs);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *w.count = have < total ? 0 : total;
+        if (have < total) set_error(w.err, kErrPages);
+    }
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+        const int L = have < total ? -1 : len[i];
+        w.val[i] = L < 0 ? -1 : L / kPage;
+        if (L < 0) continue;
+        const int a = __ldcg(parents + i), c = __ldcg(children + i);
+        p.S[c] = L;
+        if (L % kPage) {
+            const int at = off[i], page = list[at];
+            const int64_t place = L / kPage;
+            w.pairs[at] = make_int2(__ldcg(p.page_table + (int64_t)a * p.pages_per_seq + place), page);
+            p.page_table[(int64_t)c * p.pages_per_seq + place] = page;
+            p.refs[page] = 1;
         }
     }
 }
 
-// One warp per listed sequence.  A sequence listed twice is freed once: each
+// One CTA per listed sequence.  A sequence listed twice is freed once: each
 // place of its table row is taken by one exchange.
-__global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* seqs, int n, wedlm_kv_pages p, int* err) {
+__global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* seqs, wedlm_kv_pages p, int* err) {
     griddep_wait();
-    const int lane = threadIdx.x & 31, i = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (i >= n) return;
-    const int q = __ldcg(seqs + i);
+    const int q = __ldcg(seqs + blockIdx.x);
     if (q < 0 || q >= p.n_seq) {
-        if (lane == 0) set_error(err, kErrBounds);
+        if (threadIdx.x == 0) set_error(err, kErrBounds);
         return;
     }
     int32_t* row = p.page_table + (int64_t)q * p.pages_per_seq;
-    for (int j = lane; j < p.pages_per_seq; j += 32) {
+    for (int j = threadIdx.x; j < p.pages_per_seq; j += 128) {
         if (__ldcg(row + j) == -1) continue;
         const int page = atomicExch(row + j, -1);
         if (page == -1) continue;
@@ -326,7 +363,7 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* seqs, in
             set_error(err, kErrBounds);
         }
     }
-    if (lane == 0) p.S[q] = 0;
+    if (threadIdx.x == 0) p.S[q] = 0;
     __threadfence();
 }
 
@@ -384,30 +421,51 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(wedlm_
     if (threadIdx.x == 0) *w.count = moves;
 }
 
-// The planned copies in every layer, 16 KB of a page at a time, and (map !=
-// nullptr) the page tables renamed.  Bound by HBM: each byte is read and
-// written once.
-__global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(wedlm_kv_pages p, const int2* pairs, const int* count,
-                                                                  const int32_t* map, int* err) {
+// What a plan leaves for the whole GPU.
+struct MoveArgs {
+    const int2* pairs;
+    const int* count;
+    int* err;
+    const int32_t* map;                 // a compaction: new ids, or nullptr
+    const int32_t *parents, *children;  // a fork of n entries (n = 0: none)
+    const int* full;                    // the pages each of them shares, -1: none
+    int n;
+};
+
+// The planned copies in every layer, 16 KB of a page at a time; before them a
+// compaction's page tables renamed, or a fork's full pages shared.  Bound by HBM:
+// each byte is read and written once.
+__global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(wedlm_kv_pages p, MoveArgs w) {
     griddep_wait();
-    if (map) {
+    if (w.map) {
         const int64_t entries = (int64_t)p.n_seq * p.pages_per_seq;
         for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < entries;
              e += (int64_t)gridDim.x * kCopyThreads) {
             const int page = __ldcg(p.page_table + e);
             if (page == -1) continue;
-            const int to = page >= 0 && page < p.num_pages ? __ldcg(map + page) : -1;
-            if (to < 0) set_error(err, kErrBounds);  // not a page in use: left as it is
+            const int to = page >= 0 && page < p.num_pages ? __ldcg(w.map + page) : -1;
+            if (to < 0) set_error(w.err, kErrBounds);  // not a page in use: left as it is
             else if (to != page) p.page_table[e] = to;
+        }
+    }
+    for (int i = blockIdx.x; i < w.n; i += gridDim.x) {
+        const int full = __ldcg(w.full + i);
+        if (full <= 0) continue;
+        const int32_t* from = p.page_table + (int64_t)__ldcg(w.parents + i) * p.pages_per_seq;
+        int32_t* to = p.page_table + (int64_t)__ldcg(w.children + i) * p.pages_per_seq;
+        for (int j = threadIdx.x; j < full; j += kCopyThreads) {
+            const int page = __ldcg(from + j);
+            to[j] = page;
+            atomicAdd(p.refs + page, 1);
         }
     }
     const int64_t nvec = p.page_bytes / 16;
     const int64_t chunks = (nvec + kCopyThreads * kCopyVec - 1) / (kCopyThreads * kCopyVec);
-    const int64_t per_pair = chunks * p.n_layers, units = per_pair * __ldcg(count);
+    const int64_t per_pair = chunks * p.n_layers, units = per_pair * __ldcg(w.count);
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int64_t k = u / per_pair, rest = u - k * per_pair;
         const int64_t layer = rest / chunks, v0 = (rest - layer * chunks) * (kCopyThreads * kCopyVec) + threadIdx.x;
-        const int2 m = __ldcg(pairs + k);
+        const int2 m = __ldcg(w.pairs + k);
         char* base = static_cast<char*>(p.pool) + layer * p.layer_stride;
         const int4* from = reinterpret_cast<const int4*>(base + (int64_t)m.x * p.page_bytes);
         int4* to = reinterpret_cast<int4*>(base + (int64_t)m.y * p.page_bytes);
@@ -422,16 +480,16 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(wedlm_kv_pages
     __threadfence();
 }
 
-cudaError_t launch_move(const wedlm_kv_pages& p, const PagesWs& w, int64_t most, const int32_t* map, cudaStream_t st) {
+// most: how many copies there can be.
+cudaError_t launch_move(const wedlm_kv_pages& p, const MoveArgs& a, int64_t most, cudaStream_t st) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t chunks = (p.page_bytes / 16 + kCopyThreads * kCopyVec - 1) / (kCopyThreads * kCopyVec);
     int64_t units = most * p.n_layers * chunks;
-    if (map) units = std::max(units, ((int64_t)p.n_seq * p.pages_per_seq + kCopyThreads - 1) / kCopyThreads);
+    if (a.map) units = std::max(units, ((int64_t)p.n_seq * p.pages_per_seq + kCopyThreads - 1) / kCopyThreads);
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, (int64_t)sms * 8));
-    return launch_pdl(pages_move_kernel, dim3((unsigned)grid), dim3(kCopyThreads), 0, st, p, (const int2*)w.pairs,
-                      (const int*)w.count, map, w.err);
+    return launch_pdl(pages_move_kernel, dim3((unsigned)grid), dim3(kCopyThreads), 0, st, p, a);
 }
 
 // A description that the kernels can follow without leaving its buffers.
@@ -470,7 +528,7 @@ wedlm_status wedlm_kv_pages_copy(const wedlm_kv_pages* pages, const int32_t* src
     const PagesWs w = pages_ws(workspace, pages->num_pages, pages->n_seq);
     cudaError_t e = launch_pdl(pages_copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, src, dst, n,
                                pages->num_pages, w);
-    if (e == cudaSuccess) e = launch_move(*pages, w, n, nullptr, st);
+    if (e == cudaSuccess) e = launch_move(*pages, {w.pairs, w.count, w.err, nullptr, nullptr, nullptr, nullptr, 0}, n, st);
     return done(e);
 }
 
@@ -480,8 +538,8 @@ wedlm_status wedlm_kv_pages_reserve(const wedlm_kv_pages* pages, const int32_t* 
     if (n == 0) return WEDLM_OK;
     if (!seqs || !tokens) return WEDLM_ERR_INVALID_ARG;
     const PagesWs w = pages_ws(workspace, pages->num_pages, pages->n_seq);
-    return done(launch_pdl(pages_reserve_kernel, dim3(1), dim3(kPlanThreads), 0, (cudaStream_t)stream, seqs, tokens, n,
-                           *pages, w));
+    return done(launch_pdl(pages_reserve_kernel, dim3(1), dim3(kPlanThreads), sizeof(PlanLists), (cudaStream_t)stream, seqs,
+                           tokens, n, *pages, w));
 }
 
 wedlm_status wedlm_kv_pages_fork(const wedlm_kv_pages* pages, const int32_t* parents, const int32_t* children,
@@ -491,9 +549,9 @@ wedlm_status wedlm_kv_pages_fork(const wedlm_kv_pages* pages, const int32_t* par
     if (!parents || !children) return WEDLM_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     const PagesWs w = pages_ws(workspace, pages->num_pages, pages->n_seq);
-    cudaError_t e = launch_pdl(pages_fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, parents, children, n,
-                               *pages, w);
-    if (e == cudaSuccess) e = launch_move(*pages, w, n, nullptr, st);
+    cudaError_t e = launch_pdl(pages_fork_plan_kernel, dim3(1), dim3(kPlanThreads), sizeof(PlanLists), st, parents,
+                               children, n, *pages, w);
+    if (e == cudaSuccess) e = launch_move(*pages, {w.pairs, w.count, w.err, nullptr, parents, children, w.val, n}, n, st);
     return done(e);
 }
 
@@ -502,8 +560,8 @@ wedlm_status wedlm_kv_pages_free(const wedlm_kv_pages* pages, const int32_t* seq
     if (!pages_ok(pages, workspace, workspace_bytes) || n < 0 || n > pages->n_seq) return WEDLM_ERR_INVALID_ARG;
     if (n == 0) return WEDLM_OK;
     if (!seqs) return WEDLM_ERR_INVALID_ARG;
-    return done(launch_pdl(pages_free_kernel, dim3((unsigned)((n + 3) / 4)), dim3(128), 0, (cudaStream_t)stream, seqs,
-                           n, *pages, static_cast<int*>(workspace)));
+    return done(launch_pdl(pages_free_kernel, dim3((unsigned)n), dim3(128), 0, (cudaStream_t)stream, seqs, *pages,
+                           static_cast<int*>(workspace)));
 }
 
 wedlm_status wedlm_kv_pages_compact(const wedlm_kv_pages* pages, int32_t* map, void* workspace,
@@ -513,7 +571,8 @@ wedlm_status wedlm_kv_pages_compact(const wedlm_kv_pages* pages, int32_t* map, v
     const PagesWs w = pages_ws(workspace, pages->num_pages, pages->n_seq);
     int32_t* m = map ? map : w.list;
     cudaError_t e = launch_pdl(pages_compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, *pages, m, w);
-    if (e == cudaSuccess) e = launch_move(*pages, w, pages->num_pages / 2, (const int32_t*)m, st);
+    if (e == cudaSuccess)
+        e = launch_move(*pages, {w.pairs, w.count, w.err, m, nullptr, nullptr, nullptr, 0}, pages->num_pages / 2, st);
     return done(e);
 }
 
