@@ -55,11 +55,11 @@ constexpr int REGS_SOFTMAX = 144, REGS_WIDEN = 56, REGS_REST = 80;
 static_assert(8 * REGS_SOFTMAX + 8 * REGS_WIDEN + 4 * REGS_REST <= 20 * 96, "more registers than the block was launched with");
 constexpr uint32_t TM_COLS = 512;             // S_t at 128 t, O_t at 256 + 128 t
 constexpr int OFF_BUF = 0;
-constexpr int OFF_Q = OFF_BUF + NBUF * BUF_BYTES;  // ROWS: a Q per tile; else one Q and the exchange of the tiles' O
+constexpr int OFF_Q = OFF_BUF + NBUF * BUF_BYTES;  // ROWS: a Q per tile; else one Q and the exchange of the parts' O
 constexpr int OFF_RAW = OFF_Q + 2 * BUF_BYTES;
 constexpr int OFF_ITEMS = OFF_RAW + NRAW * RAW_BYTES;
-constexpr int OFF_ML = OFF_ITEMS + (int)sizeof(ItemTable);  // (m, l) of tile 1's rows
-constexpr int OFF_EX = OFF_ML + 128 * 8;                    // !ROWS: the exponents added to Q's rows
+constexpr int OFF_ML = OFF_ITEMS + (int)sizeof(ItemTable);  // !ROWS: every softmax thread's (m, l)
+constexpr int OFF_EX = OFF_ML + 256 * 8;                    // !ROWS: the exponents added to Q's rows
 constexpr int OFF_BAR = OFF_EX + 128 * 4;
 constexpr int NBARS = 2 * NRAW + 2 * NBUF + 2 * NITEM + 8 + 1;
 constexpr int OFF_FLAGS = OFF_BAR + NBARS * 8;
@@ -144,7 +144,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 bytes a thread: a thread writes whole sectors of its own row.
 // Waits for the loads issued so far; r: registers that one of them fills (tied, so
 // that no use of them moves ahead of the wait).
 __device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
@@ -157,6 +156,9 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void st_shared16(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -203,6 +205,24 @@ __device__ __forceinline__ void store_row(const AttnKv4Params& p, int nsplit, in
     }
 }
 
+// 8 dims from c on.
+__device__ __forceinline__ void store8(const AttnKv4Params& p, int nsplit, int sp, int64_t at, int c, const float (&v)[8],
+                                       float f) {
+    uint32_t r[8];
+    if (nsplit == 1) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * y] * f, v[2 * y + 1] * f);
+            r[y] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p.out + at * HD + c) = make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+#pragma unroll
+        for (int y = 0; y < 8; ++y) r[y] = __float_as_uint(v[y]);
+        st_global8(p.part_o + (at * p.max_splits + sp) * HD + c, r);
+    }
+}
+
 // Barrier among the 256 softmax threads, returning whether `v` holds in all of
 // them: steps that synchronise the tiles are entered by all or by none, also
 // when a bounded wait gave up in one warp only.
@@ -218,10 +238,10 @@ __device__ __forceinline__ bool softmax_all(bool v) {
 template <bool ROWS>
 __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Params p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);  // (an offset: the compiler still knows that it is shared memory)
     uint8_t* bufs = smem + OFF_BUF;
     uint8_t* sQ = smem + OFF_Q;
-    float* xch = reinterpret_cast<float*>(smem + OFF_Q + BUF_BYTES);  // !ROWS: 64 dims x 128 rows
+    float* xch = reinterpret_cast<float*>(smem + OFF_Q + BUF_BYTES);  // !ROWS: 32 dims x 256 threads
     uint8_t* raw = smem + OFF_RAW;
     ItemTable& items = *reinterpret_cast<ItemTable*>(smem + OFF_ITEMS);
     float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
@@ -423,9 +443,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
         // the upper dims take the token beside the others': the swizzle then sends
         // the eight lanes of a 16-byte store to eight different places.
         const int w = warp - WARP_WIDEN, blk = lane & 7, tok = (lane >> 3) ^ (blk >> 2);
-        const int ch = 2 * (blk & 3), base_off = (blk >> 2) * HALF_BYTES + tok * 128;
-        // places of the block's two 16-byte chunks, for tokens tok and tok + 4 (mod 8)
-        const int pos[2][2] = {{(ch ^ tok) << 4, ((ch + 1) ^ tok) << 4}, {(ch ^ (tok + 4)) << 4, ((ch + 1) ^ (tok + 4)) << 4}};
+        // place of the first of the block's two 16-byte chunks in token tok's row (the
+        // second's differs in bit 4, those of token tok + 4 in bit 6)
+        const uint32_t place = smem_u32(bufs) + (blk >> 2) * HALF_BYTES + (w * kPage + tok) * 128 + (((2 * (blk & 3)) ^ tok) << 4);
         uint32_t gb = 0;
         bool ok = true;
         for (uint32_t li = 0; ok; ++li) {
@@ -439,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t x = 2 * gb + kv;
-                    uint8_t* dst = bufs + (x % NBUF) * BUF_BYTES + base_off;
+                    const uint32_t dst = place + (x % NBUF) * BUF_BYTES;
                     if (!(ok = warp_wait(&buf_empty[x % NBUF], ((x / NBUF) & 1) ^ 1, err))) break;
                     const uint32_t r = 2 * gb + w / RPP;
                     if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAW], (r / NRAW) & 1, err))) break;
@@ -469,11 +489,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         uint32_t lo[4], hi[4];
                         e2m1x8_to_f16x2(code[i].x, lo);
                         e2m1x8_to_f16x2(code[i].y, hi);
-                        uint8_t* row = dst + (w * kPage + 4 * i) * 128;
-                        *reinterpret_cast<uint4*>(row + pos[i & 1][0]) =
-                            make_uint4(hmul2(lo[0], sc), hmul2(lo[1], sc), hmul2(lo[2], sc), hmul2(lo[3], sc));
-                        *reinterpret_cast<uint4*>(row + pos[i & 1][1]) =
-                            make_uint4(hmul2(hi[0], sc), hmul2(hi[1], sc), hmul2(hi[2], sc), hmul2(hi[3], sc));
+                        const uint32_t at = (i & 1 ? dst ^ 64u : dst) + 512 * i;
+                        st_shared16(at, hmul2(lo[0], sc), hmul2(lo[1], sc), hmul2(lo[2], sc), hmul2(lo[3], sc));
+                        st_shared16(at ^ 16u, hmul2(hi[0], sc), hmul2(hi[1], sc), hmul2(hi[2], sc), hmul2(hi[3], sc));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
@@ -500,9 +518,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             const int tile_rows = min(item.rows - item.q0, ROWS ? 256 : 128);
             const bool twice = !ROWS && tile_rows <= 64;  // rows repeated on lanes 64 .. 127
             const int row = ROWS ? (int)threadIdx.x : twice ? lane_row & 63 : lane_row;
-            // rows this thread works for: with `twice` tile 0 the lower, tile 1 the upper lanes
-            const bool live = row < tile_rows && (!twice || (lane_row >> 6) == t);
-            const bool warp_live = !twice || ((lane_row >> 6) == t);
+            const bool live = row < tile_rows;
+            // the keys of a block this thread works on: with `twice` the lower lanes the first half
+            const int cb = twice ? lane_row & 64 : 0, ce = twice ? cb + 64 : KBLK;
             const int qr = item.q0 + min(row, tile_rows - 1);
             const int64_t at = ((int64_t)item.b * p.stride + qr / g) * p.hq + item.h * g + qr % g;
             // Q by the tile that owns it: each thread brings its row to the row's place in
@@ -559,14 +577,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             for (int j = ROWS ? 0 : t; j < nblk; j += ROWS ? 1 : 2, ++x) {
                 if (!(ok = warp_wait(&s_full[t], x & 1, err))) break;
                 tc_fence_after();
-                if (warp_live) {
+                {
                     const int key0 = ks + j * KBLK;
                     const int gone = flags[(base + j) % FLAGS];  // (written before the block's K was)
                     // (Loops are kept rolled: four roles share the instruction cache.)
                     if (key0 + KBLK - 1 > all || gone) {
                         // scores of keys that are not visible to -inf, in place
 #pragma unroll 1
-                        for (int c = 0; c < KBLK; c += 32) {
+                        for (int c = cb; c < ce; c += 32) {
                             uint32_t r[32];
                             tmem_ld32(tS + c, r);
                             tmem_wait_ld(r);
@@ -586,14 +604,14 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         for (int y = 0; y < 32; y += 2)
                             mx[(y >> 1) & 3] = max3(mx[(y >> 1) & 3], __uint_as_float(r[y]), __uint_as_float(r[y + 1]));
                     };
-                    tmem_ld32(tS, ra);
+                    tmem_ld32(tS + cb, ra);
 #pragma unroll 1
-                    for (int c = 0; c < KBLK; c += 64) {
+                    for (int c = cb; c < ce; c += 64) {
                         tmem_wait_ld(ra);
                         tmem_ld32(tS + c + 32, rb);
                         take_max(ra);
                         tmem_wait_ld(rb);
-                        tmem_ld32(tS + (c + 64) % KBLK, ra);  // (at last the first ones again, for the weights)
+                        tmem_ld32(tS + (c + 64 < ce ? c + 64 : cb), ra);  // (at last the first ones again, for the weights)
                         take_max(rb);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -635,13 +653,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         tmem_st16(tS + c, pk);
                     };
 #pragma unroll 1
-                    for (int c = 0; c < KBLK; c += 64) {
+                    for (int c = cb; c < ce; c += 64) {
                         tmem_wait_ld(ra);
                         tmem_ld32(tS + c + 32, rb);
                         weigh(c, ra);
                         tmem_wait_ld(rb);
-                        if (c + 64 < KBLK) tmem_ld32(tS + c + 64, ra);
+                        if (c + 64 < ce) tmem_ld32(tS + c + 64, ra);
                         weigh(c + 32, rb);
+                    }
+                    if (!ROWS && twice) {  // the other half's keys weigh nothing in this row of P
+                        uint32_t zero[16] = {};
+                        tmem_st16(tS + 64 - cb, zero);
+                        tmem_st16(tS + 96 - cb, zero);
                     }
                     const float2 both = unpair(add2(sum[0], sum[1]));
                     l += both.x + both.y;
@@ -669,44 +692,43 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                 }
                 if (live && nsplit > 1) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
             } else {
-                // tile 1's result joins tile 0's: O = 2^(m0 - M) O0 + 2^(m1 - M) O1, M = max(m0, m1)
-                if (t == 1 && live) s_ml[row] = make_float2(m, l);
+                // A row's 2 (`twice`: 4) parts, of the threads that lie `step` apart, joined:
+                // O = sum of 2^(m_i - M) O_i, M the largest m_i.  Of every 32 dims each of
+                // those threads adds up and stores its share.
+                const int step = twice ? 64 : 128, mine = (int)threadIdx.x & (step - 1);
+                s_ml[threadIdx.x] = make_float2(m, l);
                 if (!(ok = softmax_all(ok))) break;
-                float f = 0.f, f1 = 0.f;
-                if (t == 0 && live) {
-                    const float2 o = s_ml[row];
-                    const float M = fmaxf(m, o.x);
-                    f = m == -INFINITY ? 0.f : exp2_fast(m - M);
-                    f1 = o.x == -INFINITY ? 0.f : exp2_fast(o.x - M);
-                    l = f * l + f1 * o.y;
-                    m = M;
+                float M = -INFINITY, L = 0.f;
+                for (int x = mine; x < 256; x += step) M = fmaxf(M, s_ml[x].x);
+                for (int x = mine; x < 256; x += step) {
+                    const float2 o = s_ml[x];
+                    L += (o.x == -INFINITY ? 0.f : exp2_fast(o.x - M)) * o.y;  // (NaN stays NaN)
                 }
-                const float inv = out_factor(p.v_scale, l);
+                const float f = any && m > -INFINITY ? exp2_fast(m - M) : 0.f, inv = out_factor(p.v_scale, L);
 #pragma unroll 1
                 for (int c = 0; c < HD; c += 32) {
                     uint32_t r[32];
-                    // (warps whose lanes have nothing to do skip the load)
-                    if (any && warp_live) {
+                    if (any) {
                         tmem_ld32(tO + c, r);
                         tmem_wait_ld(r);
                     }
-                    float* x_row = xch + (c & 32) * 128 + row;
-                    if (t == 1 && live) {
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) x_row[y * 128] = any ? __uint_as_float(r[y]) : 0.f;
+                    for (int y = 0; y < 32; ++y) xch[y * 256 + threadIdx.x] = f > 0.f ? f * __uint_as_float(r[y]) : 0.f;
+                    if (!(ok = softmax_all(ok))) break;
+                    const int share = step / 8, d0 = ((int)threadIdx.x / step) * share;  // 32 dims / (256 / step) threads
+#pragma unroll 1
+                    for (int d = d0; live && d < d0 + share; d += 8) {
+                        float v[8] = {};
+#pragma unroll 2
+                        for (int x = mine; x < 256; x += step)
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) v[y] += xch[(d + y) * 256 + x];
+                        store8(p, nsplit, sp, at, c + d, v, inv);
                     }
                     if (!(ok = softmax_all(ok))) break;
-                    if (t == 0 && live) {
-#pragma unroll
-                        for (int y = 0; y < 32; ++y) {
-                            const float own = f > 0.f ? f * __uint_as_float(r[y]) : 0.f;
-                            r[y] = __float_as_uint(f1 > 0.f ? fmaf(f1, x_row[y * 128], own) : own);
-                        }
-                        store_row(p, nsplit, sp, at, c, r, inv);
-                    }
                 }
                 if (!ok) break;
-                if (t == 0 && live && nsplit > 1) p.part_ml[at * p.max_splits + sp] = make_float2(m, l);
+                if ((int)threadIdx.x < step && live && nsplit > 1) p.part_ml[at * p.max_splits + sp] = make_float2(M, L);
             }
             tc_fence_before();
         }
