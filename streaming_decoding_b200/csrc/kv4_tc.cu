@@ -6,9 +6,9 @@
 // for the CTA's two tiles t.  ROWS: the tiles are the two halves of 256 query
 // rows and every block serves both.  Otherwise (at most 128 query rows) the
 // tiles hold the same rows and take the blocks in turn, each with its own
-// maximum, sum and O, joined at the item's end; with at most 64 rows tile 1's
-// rows are repeated on lanes 64 .. 127 and only those are worked on, so that the
-// two tiles' softmax runs on different schedulers.  Operands are fp16: a code
+// maximum, sum and O, joined at the item's end; with at most 64 rows they are
+// repeated on lanes 64 .. 127, which weigh the second half of a block's keys as
+// the lower lanes do the first, so that all warps share the softmax.  Operands are fp16: a code
 // times its scale is exact in it, Q is scaled per row by a power of two and P is
 // relative to a lazily raised maximum, as in kv4.cu.
 //
@@ -17,10 +17,19 @@
 // thread after 220, so few and large steps.  Two tiles, because one's softmax
 // (at least 1024 cycles of the exp2 unit a block) then runs under the other's
 // products (1040).  A block and tile pair costs the tensor pipe 2080 cycles
-// (ROWS), the shared memory's bandwidth about 2300.
+// (ROWS), the shared memory's bandwidth about 2300, and takes 4300: a tile's
+// chain of S (810 until a softmax warp sees it), softmax (2580) and P V (890 until
+// the next S may start, which overwrites P) is what bounds it.  With the softmax
+// left out it took 3500, with the widening's stores left out too 3400 (the MMA
+// thread's own chain of products and commits); 16 softmax warps, which share the
+// same schedulers, were no faster, an MMA thread for each tile slower (456 us:
+// products of both tiles alternate in the pipe).
+//   64 sequences at 8.2k to 8.7k, windows of 32, 7 heads to a KV head: 331 us,
+//   586 TFLOP/s (mma.sync items of 16 rows: 1180); 16 sequences of 128 to 2047,
+//   windows of 16, 4 heads: 30 us (51), of which the start takes 5 and the end 3.
 //
 // Persistent, one CTA to an SM.  Warps:
-//   8  softmax: thread i of tile t owns query row i (a TMEM lane): Q to shared
+//   8  softmax: thread i of tile t owns lane i of TMEM, a query row: Q to shared
 //      memory, S to P in place, O rescaled when its maximum grows by more than
 //      2^8, O read out at an item's end,
 //   8  widen: warp w takes page w of every block from the ring of raw pages to
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
     uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // [NRAW] a block's pages are there
     uint64_t* raw_empty = raw_full + NRAW;                             // [NRAW] read (a warp a page)
     uint64_t* buf_full = raw_empty + NRAW;                             // [NBUF] K or V widened (8 warps)
-    uint64_t* buf_empty = buf_full + NBUF;                             // [NBUF] its products done (by each tile it serves)
+    uint64_t* buf_empty = buf_full + NBUF;                             // [NBUF] its products done (of both tiles that it serves)
     uint64_t* q_full = buf_empty + NBUF;                               // [2] an item's Q is there (4 warps)
     uint64_t* s_full = q_full + 2;                                     // [2] S of a tile's block done
     uint64_t* p_full = s_full + 2;                                     // [2] P written (4 warps)
@@ -270,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
         }
         for (int s = 0; s < NBUF; ++s) {
             mbar_init(&buf_full[s], PPB);
-            mbar_init(&buf_empty[s], ROWS ? 2 : 1);
+            mbar_init(&buf_empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 4);
@@ -381,10 +390,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             constexpr uint64_t BUF16 = BUF_BYTES >> 4, HALF16 = HALF_BYTES >> 4;
             auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_short(bar, parity, err); };
             // (A look at a barrier takes over a hundred cycles beside the widening's
-            // stores, so the widened block is waited for before what it waits for anyway.)
+            // stores: a widened block is waited for before what it waits for anyway, and
+            // ROWS by tile 0 alone; tile 1, whose products come later, lets it go.)
             auto issue_s = [&](int t, uint32_t b, uint64_t* after, uint32_t after_parity) {
                 const uint32_t kx = 2 * b;
-                if (!wait(&buf_full[kx % NBUF], (kx / NBUF) & 1) || !wait(after, after_parity)) return;
+                if ((!ROWS || t == 0) && !wait(&buf_full[kx % NBUF], (kx / NBUF) & 1)) return;
+                if (!wait(after, after_parity)) return;
                 tc_fence_after();
                 const uint64_t q = dq + (ROWS ? t : 0) * BUF16, k = dk + (kx % NBUF) * BUF16;
 #pragma unroll
@@ -392,11 +403,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                     mma_ss(tmem + 128 * t, q + (kk >> 2) * HALF16 + (kk & 3) * 2, k + (kk >> 2) * HALF16 + (kk & 3) * 2, idS,
                            kk > 0 ? 1u : 0u);
                 umma_commit(&s_full[t]);
-                umma_commit(&buf_empty[kx % NBUF]);
+                if (!ROWS || t == 1) umma_commit(&buf_empty[kx % NBUF]);
             };
             auto issue_pv = [&](int t, uint32_t b, bool first) {
                 const uint32_t vx = 2 * b + 1;
-                if (!wait(&buf_full[vx % NBUF], (vx / NBUF) & 1) || !wait(&p_full[t], (xs >> t) & 1)) return;
+                if ((!ROWS || t == 0) && !wait(&buf_full[vx % NBUF], (vx / NBUF) & 1)) return;
+                if (!wait(&p_full[t], (xs >> t) & 1)) return;
                 tc_fence_after();
                 const uint64_t v = dv + (vx % NBUF) * BUF16;
 #pragma unroll
@@ -404,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                     mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + (kk >> 1) * 32 + (kk & 1) * 8, v + kk * 128, idO,
                            (!first || kk > 0) ? 1u : 0u);
                 umma_commit(&pv_done[t]);
-                umma_commit(&buf_empty[vx % NBUF]);
+                if (!ROWS || t == 1) umma_commit(&buf_empty[vx % NBUF]);
             };
             for (uint32_t li = 0; ok; ++li) {
                 if (!wait(&item_full[li % NITEM], (li / NITEM) & 1)) break;
