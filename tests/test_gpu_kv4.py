@@ -78,6 +78,68 @@ def test_rows_match_the_definition(hkv, stride, S, n, scales, dtype):
     assert int(err) == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_and_an_odd_number_of_heads(dtype):
+    """Launches of thousands of rows give a lane several blocks: 3 heads leave some of them without one."""
+    test_rows_match_the_definition(3, 1400, [0, 5, 100], [1400, 1300, 7], (1.0, 0.5), dtype)
+
+
+def test_every_bf16_quotient_rounds_as_the_definition():
+    """Blocks of every largest significand with every bf16 value from it down to 2^-6 of it, in the scales'
+    normal and subnormal range: quotients halfway between two codes, and next to it."""
+    from streaming_decoding_b200 import kv4_append
+    sig = (128 + np.arange(128)) / 128.0
+    vals = np.concatenate([sig * 2.0 ** -e for e in range(6)])
+    blocks = []
+    for top in sig:
+        v = np.where(vals <= top, vals, vals / 2)
+        v = np.append(v, np.zeros(-len(v) % 15)).reshape(-1, 15)
+        blocks.append(np.concatenate([np.full((len(v), 1), top), v * np.where(np.arange(15) % 2, 1, -1)], 1))
+    x = np.concatenate(blocks)
+    x = np.concatenate([x, x * 2.0 ** -5, x * 2.0 ** -7, x * 2.0 ** 11]).reshape(-1, 1, 128)
+    m = len(x)
+    xt = torch.from_numpy(x).to(torch.bfloat16).cuda()
+    assert np.array_equal(xt.double().cpu().numpy(), x)
+    for g in (1.0, 2.0 ** 20, 2.0 ** -30):
+        pages = (m + 15) // 16
+        pool = torch.zeros(pages, 1, 2, R.HALF, dtype=torch.uint8, device="cuda")
+        err = i32([0])
+        y = xt * g  # exact
+        kv4_append(y, y, pool, torch.arange(pages, dtype=torch.int32, device="cuda")[None], i32([0]), i32([m]), m, err, g, g)
+        codes, scales = R.encode(x, 1.0)
+        got = pool.cpu().numpy()
+        for which in range(2):
+            c = got[:, 0, which, :1024].reshape(-1, 64)[:m]
+            assert np.array_equal(got[:, 0, which, 1024:].reshape(-1, 8)[:m], scales[:, 0])
+            for sh in (0, 4):
+                a, b = c >> sh & 15, codes[:, 0] >> sh & 15
+                assert ((a == b) | ((a & 7 == 0) & (b & 7 == 0))).all()
+        assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m", [5, 4100])
+def test_rows_on_sixteen_byte_boundaries(dtype, m):
+    """Rows whose start is no multiple of 32 bytes: the same bytes in, the same values out."""
+    from streaming_decoding_b200 import kv4_append, kv4_pool, kv4_read
+    off = 16 // dtype.itemsize
+    x = torch.randn(2, m, 2, 128, device="cuda").to(dtype)
+    odd = torch.empty(2, m * (256 + off) + off, dtype=dtype, device="cuda")
+    views = [o[off:].unflatten(0, (m, 256 + off))[:, :256].unflatten(1, (2, 128)) for o in odd]
+    for view, src in zip(views, x):
+        view.copy_(src)
+    assert views[0].data_ptr() % 32 == 16 and views[0].stride(0) * dtype.itemsize % 32 == 16
+    pages = (m + 15) // 16
+    table, err = torch.randperm(pages, device="cuda").int()[None], i32([0])
+    pools = [kv4_pool(pages, 2) for _ in range(2)]
+    kv4_append(x[0], x[1], pools[0], table, i32([0]), i32([m]), m, err)
+    kv4_append(views[0], views[1], pools[1], table, i32([0]), i32([m]), m, err)
+    assert torch.equal(pools[0], pools[1])
+    plain = kv4_read(pools[0], table, i32([0]), i32([m]), m, err, dtype=dtype)
+    kv4_read(pools[0], table, i32([0]), i32([m]), m, err, out=tuple(views))
+    assert torch.equal(views[0], plain[0]) and torch.equal(views[1], plain[1]) and int(err) == 0
+
+
 def test_rows_saturate_refuse_nonfinite_and_stay_in_bounds():
     from streaming_decoding_b200 import kv4_append, kv4_pool, kv4_read
     x = torch.zeros(4, 1, 128, device="cuda")
@@ -201,6 +263,25 @@ def test_attention_spread_of_scores(qstd):
 
 def test_attention_scales_and_many_sequences():
     attention_case(15, 8, 2, 2, list(range(0, 130)), [1, 2] * 65, scales=(4.0, 2.0 ** -10))
+
+
+@pytest.mark.parametrize("rows", [17, 64, 65, 128, 129, 256, 257])
+@pytest.mark.parametrize("S,max_ctx", [([0, 100, 130], None), ([700, 1, 2000], 60000)])
+def test_attention_row_counts_around_the_tiles(rows, S, max_ctx):
+    """One KV head and one query head: window rows are the tile's rows; whole and divided keys."""
+    attention_case(23, 1, 1, rows, S, [rows, rows - 1, 16], max_ctx=max_ctx)
+
+
+def test_attention_more_sequences_than_the_item_table_holds():
+    rng = np.random.default_rng(24)
+    S, n = rng.integers(0, 200, 300).tolist(), rng.integers(0, 9, 300).tolist()
+    attention_case(24, 8, 2, 8, S, n)
+    attention_case(25, 8, 2, 8, S, n, max_ctx=3000)
+
+
+@pytest.mark.parametrize("stride", [1, 4, 16, 80])
+def test_attention_of_empty_windows(stride):
+    attention_case(26, 8, 2, stride, [0, 50, 3], [0, 0, 0])
 
 
 def test_attention_far_pages():

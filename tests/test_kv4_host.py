@@ -89,6 +89,11 @@ def test_attention_refusals(bad):
     assert attention(**bad) == BAD
 
 
+def test_limits_that_alignment_and_grids_set():
+    assert attention(out=P + 16) == BAD
+    assert append(hkv=65536, ks=65536 * 128, vs=65536 * 128) == BAD and read(hkv=65536, ks=65536 * 128, vs=65536 * 128) == BAD
+
+
 def test_workspace_sizes():
     lib, nb = _lib.load(), ctypes.c_int64()
     assert lib.wedlm_attention_kv4_workspace_bytes(1, 1, 32, 8, 64, ctypes.byref(nb)) == 0 and nb.value >= 256
