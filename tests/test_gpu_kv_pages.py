@@ -59,6 +59,35 @@ def test_copy_skips_entries_that_break_its_rules():
         assert ref.error == 1
 
 
+@pytest.mark.parametrize("n", [1, 4, 5, 40])
+def test_copy_of_little_and_of_much(n):
+    """Around the 128 KB up to which one kernel plans and copies (16 KB pages in two layers), refused entries among them."""
+    ref, kp = setup(10, [40], 2, 100, 6, 2, (2, 2, 16, 64))
+    src, dst = list(range(n)), list(range(50, 50 + n))
+    if n > 3:
+        dst[2], src[1] = dst[3], 1000
+    ref.copy(src, dst)
+    kp.copy(i32(src), i32(dst))
+    same(ref, kp)
+
+
+def test_more_sequences_than_the_shared_lists_hold():
+    ref, kp = setup(30, [17, 16, 40] * 500, 3001, 4000, 5, 1, (1, 1, 1, 4))
+    parents, children = list(range(1500)) + [7], list(range(1500, 3000)) + [8]
+    ref.fork(parents, children)
+    kp.fork(i32(parents), i32(children))
+    tokens = [50 + i % 30 for i in range(1500)]
+    ref.reserve(children[:1500], tokens)
+    kp.reserve(i32(children[:1500]), i32(tokens))
+    same(ref, kp)
+    assert ref.error == 1
+    ref.free(children[:1500])
+    kp.free(i32(children[:1500]))
+    ref.compact()
+    kp.compact()
+    same(ref, kp)
+
+
 @pytest.mark.parametrize("tokens", [[0, 0], [1, 48], [49, 96], [96, 16], [17, 33]])
 def test_reserve(tokens):
     ref, kp = setup(3, [40, 0, 16], 4, 30, 6)
