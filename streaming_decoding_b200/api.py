@@ -7,6 +7,7 @@ device memory and streams)."""
 from __future__ import annotations
 
 import ctypes
+import math
 
 import numpy as np
 
@@ -378,7 +379,7 @@ def _want(cond, what):
 
 def _on(t, index, dtype, shape, name):
     """A contiguous tensor of the given dtype and shape on CUDA device `index`."""
-    if t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name}: wants a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -395,7 +396,7 @@ def _launch(name, index, stream, *args):
     import torch
     fn = getattr(_lib.load(), name)
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(index):
@@ -422,15 +423,24 @@ def kv4_pool(num_pages: int, n_kv_heads: int, n_layers: int | None = None, devic
 
 def _kv4_args(kv4_pool, page_table, S, n, index):
     import torch
-    half = C["WEDLM_KV4_HALF_PAGE"]
-    pool, n_seq = kv4_pool.shape, page_table.shape[0]
-    _want(len(pool) == 4 and pool[2] == 2 and pool[3] == half, f"kv4_pool: wants [pages, kv heads, 2, {half}]")
-    _want(page_table.dim() == 2, "page_table: wants [n_seq, pages_per_seq]")
-    _on(kv4_pool, index, torch.uint8, pool, "kv4_pool")
-    _on(page_table, index, torch.int32, page_table.shape, "page_table")
-    _on(S, index, torch.int32, (n_seq,), "S")
-    _on(n, index, torch.int32, (n_seq,), "n")
-    return n_seq, pool[0], pool[1]
+    half, int32 = C["WEDLM_KV4_HALF_PAGE"], torch.int32
+    pool, table = kv4_pool.shape, page_table.shape
+    if len(pool) != 4 or pool[2] != 2 or pool[3] != half:
+        raise ValueError(f"kv4_pool: wants [pages, kv heads, 2, {half}]")
+    if len(table) != 2:
+        raise ValueError("page_table: wants [n_seq, pages_per_seq]")
+    n_seq, width = table
+    per_seq = (n_seq,)
+    # (one test of all that `_on` tests, then the argument that fails)
+    if (kv4_pool.dtype is not torch.uint8 or page_table.dtype is not int32 or S.dtype is not int32 or n.dtype is not int32
+            or S.shape != per_seq or n.shape != per_seq or kv4_pool.get_device() != index
+            or page_table.get_device() != index or S.get_device() != index or n.get_device() != index
+            or not (kv4_pool.is_contiguous() and page_table.is_contiguous() and S.is_contiguous() and n.is_contiguous())):
+        _on(kv4_pool, index, torch.uint8, pool, "kv4_pool")
+        _on(page_table, index, int32, table, "page_table")
+        _on(S, index, int32, per_seq, "S")
+        _on(n, index, int32, per_seq, "n")
+    return n_seq, width, pool[0], pool[1]
 
 
 def _rows_arg(t, rows, hkv, index, dtype, name):
@@ -445,16 +455,19 @@ def _rows_arg(t, rows, hkv, index, dtype, name):
 
 def _rows_dtype(dtype):
     import torch
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return C["WEDLM_DTYPE_F32"]
-    _want(dtype == torch.bfloat16, f"rows are float32 or bfloat16, got {dtype}")
-    return C["WEDLM_DTYPE_BF16"]
+    if dtype is torch.bfloat16:
+        return C["WEDLM_DTYPE_BF16"]
+    raise ValueError(f"rows are float32 or bfloat16, got {dtype}")
 
 
 def _error_word(t, index):
     import torch
-    _want(t.get_device() == index and t.is_contiguous() and t.dtype in (torch.int32, torch.uint8) and
-          t.numel() * t.element_size() >= 4, "error: wants an int32 tensor or a workspace on the same device")
+    dtype = t.dtype
+    if (t.get_device() != index or not t.is_contiguous() or
+            t.numel() < (1 if dtype is torch.int32 else 4 if dtype is torch.uint8 else math.inf)):
+        raise ValueError("error: wants an int32 tensor or a workspace on the same device")
 
 
 def kv4_append(k, v, kv4_pool, page_table, S, n, stride: int, error, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -465,13 +478,13 @@ def kv4_append(k, v, kv4_pool, page_table, S, n, stride: int, error, k_scale: fl
     pages_per_seq], S, n [n_seq] int32; error: an int32 tensor, or the workspace
     of attention_kv4, whose first word records errors (attention_error)."""
     index = _index(k, "k")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
+    n_seq, width, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
     dtype = k.dtype
     ks = _rows_arg(k, n_seq * stride, hkv, index, dtype, "k")
     vs = _rows_arg(v, n_seq * stride, hkv, index, dtype, "v")
     _error_word(error, index)
     _launch("wedlm_kv4_append", index, stream, k.data_ptr(), v.data_ptr(), _rows_dtype(dtype), ks, vs,
-            kv4_pool.data_ptr(), pages, hkv, page_table.data_ptr(), page_table.shape[1], S.data_ptr(), n.data_ptr(),
+            kv4_pool.data_ptr(), pages, hkv, page_table.data_ptr(), width, S.data_ptr(), n.data_ptr(),
             n_seq, stride, k_scale, v_scale, error.data_ptr())
 
 
@@ -481,7 +494,7 @@ def kv4_read(kv4_pool, page_table, S, n, stride: int, error, dtype=None, k_scale
     [n_seq*stride, n_kv_heads, 128] in dtype (bfloat16 unless given), or written
     into out = (k, v).  Rows r >= n[b] are left as they are."""
     index = _index(kv4_pool, "kv4_pool")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
+    n_seq, width, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
     if out is None:
         import torch
         out = tuple(_empty_on(stream, index, (n_seq * stride, hkv, 128), dtype or torch.bfloat16) for _ in range(2))
@@ -492,7 +505,7 @@ def kv4_read(kv4_pool, page_table, S, n, stride: int, error, dtype=None, k_scale
     vs = _rows_arg(v, n_seq * stride, hkv, index, dtype, "v")
     _error_word(error, index)
     _launch("wedlm_kv4_read", index, stream, kv4_pool.data_ptr(), pages, hkv, page_table.data_ptr(),
-            page_table.shape[1], S.data_ptr(), n.data_ptr(), n_seq, stride, k_scale, v_scale, k.data_ptr(),
+            width, S.data_ptr(), n.data_ptr(), n_seq, stride, k_scale, v_scale, k.data_ptr(),
             v.data_ptr(), _rows_dtype(dtype), ks, vs, error.data_ptr())
     return k, v
 
@@ -515,7 +528,7 @@ def attention_kv4(q, kv4_pool, page_table, S, n, stride: int, n_heads: int, n_kv
     read attention_error(workspace) after synchronising."""
     import torch
     index = _index(q, "q")
-    n_seq, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
+    n_seq, width, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)
     _want(hkv == n_kv_heads, "kv4_pool has another number of KV heads")
     shape = (n_seq * stride, n_heads, 128)
     _on(q, index, torch.bfloat16, shape, "q")
@@ -525,7 +538,7 @@ def attention_kv4(q, kv4_pool, page_table, S, n, stride: int, n_heads: int, n_kv
         _on(out, index, torch.bfloat16, shape, "out")
     _on(workspace, index, torch.uint8, workspace.shape, "workspace")
     _launch("wedlm_attention_kv4", index, stream, q.data_ptr(), kv4_pool.data_ptr(), pages, n_heads, hkv,
-            page_table.data_ptr(), page_table.shape[1], S.data_ptr(), n.data_ptr(), n_seq, stride, max_ctx, k_scale,
+            page_table.data_ptr(), width, S.data_ptr(), n.data_ptr(), n_seq, stride, max_ctx, k_scale,
             v_scale, out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
