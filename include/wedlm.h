@@ -497,8 +497,9 @@ wedlm_status wedlm_attention_bf16(const void* q, const void* kv_pool, int32_t nu
  *              (WEDLM_DTYPE_F32 or WEDLM_DTYPE_BF16; others:
  *              WEDLM_ERR_UNSUPPORTED), row b * stride + r, k_stride / v_stride
  *              elements from one row to the next (at least n_kv_heads * 128, so
- *              columns of a fused projection can be given; n_kv_heads <= 65535); pointers 16-byte
+ *              columns of a fused projection can be given); pointers 16-byte
  *              aligned and strides multiples of 16 bytes.  K after RoPE.
+ *              n_kv_heads at most 65535, n_seq * stride below 2^31.
  *   S, n       DEVICE int32 [n_seq].  Rows r >= n[b] are not touched.
  *   error_word DEVICE int32, set and never cleared by the calls (the first word
  *              of a wedlm_attention_kv4 workspace may serve): 1 a position
