@@ -314,7 +314,7 @@ cudaError_t launch_read(const RowsParams& p, void* k, void* v, cudaStream_t st) 
 // outputs are fp32.
 //
 // Measured: 64 sequences of 1k to 8.2k keys, one row of 32 heads over 8 KV heads:
-// 97 us, 3.4 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
+// 94 us, 3.6 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
 // shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 62 %
 // busy: of the 20 warps that an SM's registers allow 14 are there on average, the
 // others end, start, or have no item left.  1 sequence of 256: 8.3 us, latency.
@@ -411,12 +411,14 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
     griddep_launch();
     const int lane = threadIdx.x, c = lane & 3, j8 = lane >> 2;
     const int g = p.hq / p.hkv;
+    // All sequences' first chunks, then their second ones, ...: items beyond a
+    // sequence's end come last (chunks of a sequence in a row: 97 us for 94).
     int64_t id = blockIdx.x;
     const int tile = (int)(id % p.tiles);
     id /= p.tiles;
-    const int sp = (int)(id % p.max_splits);
-    id /= p.max_splits;
-    const int h = (int)(id % p.hkv), b = (int)(id / p.hkv);
+    const int h = (int)(id % p.hkv);
+    id /= p.hkv;
+    const int b = (int)(id % p.n_seq), sp = (int)(id / p.n_seq);
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
     const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
     const int ks = sp * p.chunk, page0 = ks / kPage;
