@@ -369,6 +369,54 @@ def test_streams_and_graphs():
     assert not torch.equal(want, good)
 
 
+def test_rows_and_attention_captured_together_and_two_calls_at_once():
+    """A step's rows, attention over them and the rows read back in one graph, replayed on new inputs beside the
+    same calls of another stream with a workspace of their own."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace, kv4_append, kv4_pool, kv4_read
+    hkv, hq, W, b = 2, 8, 20, 3
+    S, n = i32([700, 5, 0]), i32([20, 7, 0])
+    table = torch.randperm(3 * 50, device="cuda").int().view(3, 50)
+
+    def side():
+        pool = kv4_pool(150, hkv)
+        pool[..., :1024] = 0x21
+        pool[..., 1024:] = 0x30
+        k, v = (torch.zeros(b * W, hkv, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        q = torch.zeros(b * W, hq, 128, device="cuda", dtype=torch.bfloat16)
+        back = tuple(torch.zeros_like(k) for _ in range(2))
+        return dict(pool=pool, k=k, v=v, q=q, back=back, out=torch.zeros_like(q), ws=attention_kv4_workspace(b, W, hq, hkv, 800))
+
+    def step(x):
+        kv4_append(x["k"], x["v"], x["pool"], table, S, n, W, x["ws"])
+        attention_kv4(x["q"], x["pool"], table, S, n, W, hq, hkv, 800, x["ws"], out=x["out"])
+        kv4_read(x["pool"], table, S, n, W, x["ws"], out=x["back"])
+
+    one, two = side(), side()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(streams[0]):
+        step(one)
+        with torch.cuda.graph(graph, stream=streams[0]):
+            step(one)
+    torch.cuda.synchronize()
+    for seed in range(3):
+        torch.manual_seed(seed)
+        for name in ("k", "v", "q"):
+            one[name].normal_()
+            two[name].copy_(one[name])
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            step(two)
+        torch.cuda.synchronize()
+        for x, y in ((one["out"], two["out"]), (one["pool"], two["pool"]), *zip(one["back"], two["back"])):
+            assert torch.equal(x, y)
+        assert attention_error(one["ws"]) == attention_error(two["ws"]) == 0
+        assert one["out"][:20].float().abs().amin(-1).gt(0).any() and not one["out"][40:].any()
+
+
 def test_binding_refuses_what_is_not_documented():
     from streaming_decoding_b200 import attention_kv4, kv4_append, kv4_read
     (q, pool, table, S, n, stride, hq, hkv, ctx, ws, kg, vg), _ = attention_case(20, 8, 2, 2, [20], [2])
