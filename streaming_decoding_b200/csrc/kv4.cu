@@ -315,8 +315,8 @@ cudaError_t launch_read(const RowsParams& p, void* k, void* v, cudaStream_t st) 
 //
 // Measured: 64 sequences of 1k to 8.2k keys, one row of 32 heads over 8 KV heads:
 // 94 us, 3.6 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
-// shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 62 %
-// busy: of the 20 warps that an SM's registers allow 14 are there on average, the
+// shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 65 %
+// busy: of the 20 warps that an SM's registers allow 15 are there on average, the
 // others end, start, or have no item left.  1 sequence of 256: 8.3 us, latency.
 constexpr int kStep = 2;              // pages of a stage
 constexpr int kStages = 2;            // (three, at 16 warps an SM: slower)
