@@ -523,14 +523,15 @@ wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_k
  * appended; rows r >= n[b] are not written; stride <= 1024), with pointers
  * 16-byte aligned, out 32-byte and the workspace 256-byte aligned, from
  * wedlm_attention_kv4_workspace_bytes.  The workspace's first int32 is the
- * device error word.  Zero the whole workspace once: calls leave its counters as
- * they found them and only ever set the error word (1: a page id outside
- * [0, num_pages), whose 16 keys are then left out, or S[b] + n[b] > max_ctx or
- * S[b] < 0, whose rows are not written; 2: a bounded wait gave up).  The cache
- * enters the products unrounded; q and the softmax weights are rounded to 11
- * significant bits, sums are fp32.  Results do not depend on other sequences.
- * Asynchronous on `stream`; no allocation.  Calls that may overlap need a
- * workspace each. */
+ * device error word.  Zero the whole workspace once, then give it to calls of any
+ * sizes that it is large enough for, one after another, and to no other use than
+ * its error word's: calls leave its counters as they found them and only ever set
+ * the error word (1: a page id outside [0, num_pages), whose 16 keys are then left
+ * out, or S[b] + n[b] > max_ctx or S[b] < 0, whose rows are not written; 2: a
+ * bounded wait gave up).  The cache enters the products unrounded; q and the
+ * softmax weights are rounded to 11 significant bits, sums are fp32.  Results do
+ * not depend on other sequences.  Asynchronous on `stream`; no allocation.  Calls
+ * that may overlap need a workspace each. */
 wedlm_status wedlm_attention_kv4_workspace_bytes(int32_t n_seq, int32_t stride, int32_t n_heads, int32_t n_kv_heads,
                                                  int32_t max_ctx, int64_t* bytes);
 wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t num_pages, int32_t n_heads,

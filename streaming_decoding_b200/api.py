@@ -524,8 +524,9 @@ def attention_kv4(q, kv4_pool, page_table, S, n, stride: int, n_heads: int, n_kv
                   k_scale: float = 1.0, v_scale: float = 1.0, out=None, stream=None):
     """attention_bf16 over a 4-bit cache (wedlm_attention_kv4).  q and out
     [n_seq*stride, n_heads, 128] bfloat16; the cache arguments as in kv4_append;
-    workspace from attention_kv4_workspace() with the same sizes.  Returns `out`;
-    read attention_error(workspace) after synchronising."""
+    workspace from attention_kv4_workspace() with these sizes or others that
+    need as much.  Returns `out`; read attention_error(workspace) after
+    synchronising."""
     import torch
     index = _index(q, "q")
     n_seq, width, pages, hkv = _kv4_args(kv4_pool, page_table, S, n, index)

@@ -324,6 +324,11 @@ constexpr int kItemsPerSm = 48;       // (36 and 64: no faster)
 // Up to this many chunks the one that finishes last joins them, 8 lanes a row; more are
 // left to a second kernel (1 sequence of 2000, 32 chunks: 9.5 us, by the last one 13.5).
 constexpr int kTicketSplits = 8;
+// Tickets count from call to call, so they have a place in the workspace that no call, of
+// whatever sizes, uses for anything else: room for this many in front of the partial results,
+// 64 KB.  Calls with more (sequence, KV head) pairs take the second kernel (1024 sequences of
+// 1000 keys and 8 KV heads, two chunks each: 241 us with tickets, 264 with the kernel).
+constexpr int kTickets = 16384;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -670,7 +675,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
                 if (j8 == 0) p.part_ml[at * p.max_splits + sp] = make_float2(m[t][x], l[t][x]);
             }
         }
-    if (nsplit == 1 || p.max_splits > kTicketSplits) return;
+    if (nsplit == 1 || !p.tickets) return;
     // The chunk that finishes last joins them all.  The ticket counts to nsplit
     // and wraps to zero, so the workspace is as it was.
     __threadfence();
@@ -759,6 +764,7 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct AttnKv4Plan {
     int tile_rows, chunk, max_splits, tiles, sms;
+    bool ticketed;  // chunks are joined by the one that finishes last
     size_t off_ticket, off_ml, off_o, bytes;
 };
 
@@ -810,7 +816,8 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     w->max_splits = (int)(((int64_t)max_ctx + w->chunk - 1) / w->chunk);
     const size_t parts = w->max_splits > 1 ? (size_t)n_seq * stride * hq * w->max_splits : 0;
     w->off_ticket = 256;
-    w->off_ml = w->off_ticket + (!tc && w->max_splits > 1 && w->max_splits <= kTicketSplits ? round256((size_t)pairs * sizeof(unsigned)) : 0);
+    w->ticketed = !tc && w->max_splits > 1 && w->max_splits <= kTicketSplits && pairs <= kTickets;
+    w->off_ml = w->off_ticket + kTickets * sizeof(unsigned);
     w->off_o = w->off_ml + round256(parts * sizeof(float2));
     w->bytes = w->off_o + round256(parts * HD * sizeof(float));
     return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
@@ -904,7 +911,7 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     char* ws = static_cast<char*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;
     const AttnKv4Params p{(const bf16*)q, (const uint8_t*)kv4_pool, page_table, S, n, (bf16*)out,
-                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), (unsigned*)(ws + w.off_ticket), (int*)ws,
+                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), w.ticketed ? (unsigned*)(ws + w.off_ticket) : nullptr, (int*)ws,
                           num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
                           w.tile_rows, w.tiles, k_scale, v_scale};
     const bool tc = w.tile_rows > 16;
@@ -912,7 +919,7 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     cudaError_t e = tc                  ? launch_attn_kv4_tc(p, w.sms, st)
                     : w.tile_rows == 8 ? launch_pdl(attn_kv4_kernel<1>, grid, dim3(32), 0, st, p)
                                        : launch_pdl(attn_kv4_kernel<2>, grid, dim3(32), 0, st, p);
-    if (e == cudaSuccess && w.max_splits > (tc ? 1 : kTicketSplits))
+    if (e == cudaSuccess && w.max_splits > 1 && !w.ticketed)
         e = launch_pdl(attn_kv4_join_kernel, dim3((unsigned)((int64_t)n_seq * stride * n_heads)),
                        dim3((w.max_splits + 31) / 32 * 32), 0, st, p);
     return e == cudaSuccess ? WEDLM_OK : WEDLM_ERR_CUDA;

@@ -1,0 +1,58 @@
+"""The 4-bit cache on the GPU beyond one call's sizes: workspaces that calls of other sizes have used."""
+import numpy as np
+import pytest
+
+import _kv4_ref as R
+from test_gpu_kv4 import dev, i32
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def test_one_workspace_serves_calls_of_all_sizes():
+    """A workspace zeroed once, large enough for every call: chunks joined by the last one, by a second kernel
+    and not divided at all, for several numbers of sequences, in turn."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    hq, hkv, pages = 32, 8, 64
+    rng = np.random.default_rng(40)
+    codes, scales = R.encode(rng.standard_normal((pages, hkv, 2, 16, 128)), 1.0)
+    raw = np.concatenate([codes.reshape(pages, hkv, 2, -1), scales.reshape(pages, hkv, 2, -1)], -1)
+    pool = dev(raw)
+    calls = []
+    for n_seq, stride, ctx in ((1, 1, 512), (1, 1, 4096), (64, 1, 512), (32, 1, 512), (3, 4, 500), (2, 16, 4000), (2, 80, 4000),
+                               (1, 1, 60)):
+        S = i32(rng.integers(ctx // 2, ctx - stride + 1, n_seq).tolist())
+        n = i32([stride] * n_seq)
+        table = dev(rng.integers(0, pages, (n_seq, (ctx + 15) // 16)).astype(np.int32))
+        q = torch.randn(n_seq * stride, hq, 128, device="cuda").to(torch.bfloat16)
+        calls.append((q, pool, table, S, n, stride, hq, hkv, ctx))
+    own = [attention_kv4_workspace(c[3].numel(), c[5], hq, hkv, c[8]) for c in calls]
+    shared = torch.zeros(max(w.numel() for w in own), dtype=torch.uint8, device="cuda")
+    alone = [attention_kv4(*c, w) for c, w in zip(calls, own)]
+    order = list(range(len(calls))) * 2 + [int(i) for i in rng.integers(0, len(calls), 40)]
+    for i in order:
+        got = attention_kv4(*calls[i], shared, out=torch.full_like(alone[i], 7.0))
+        assert torch.equal(got, alone[i]), i
+    assert attention_error(shared) == 0 and all(attention_error(w) == 0 for w in own)
+
+
+def test_more_pairs_than_there_are_tickets():
+    """Two chunks each of more (sequence, KV head) pairs than the workspace has counters for: as in two calls
+    of half the sequences, up to the last bit of the output (sums in another order)."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    hkv, n_seq, pages, ctx = 8, 2060, 64, 2000
+    rng = np.random.default_rng(41)
+    codes, scales = R.encode(rng.standard_normal((pages, hkv, 2, 16, 128)), 1.0)
+    pool = dev(np.concatenate([codes.reshape(pages, hkv, 2, -1), scales.reshape(pages, hkv, 2, -1)], -1))
+    S = dev(np.where(rng.random(n_seq) < 0.05, rng.integers(1024, 1999, n_seq), rng.integers(0, 40, n_seq)).astype(np.int32))
+    n = torch.ones_like(S)
+    table = dev(rng.integers(0, pages, (n_seq, (ctx + 15) // 16)).astype(np.int32))
+    q = torch.randn(n_seq, hkv, 128, device="cuda").to(torch.bfloat16)
+    outs = []
+    for parts in (1, 2):
+        m = n_seq // parts
+        ws = attention_kv4_workspace(m, 1, hkv, hkv, ctx)
+        outs.append(torch.cat([attention_kv4(q[x], pool, table[x], S[x], n[x], 1, hkv, hkv, ctx, ws)
+                               for x in (slice(i * m, (i + 1) * m) for i in range(parts))]).double())
+        assert attention_error(ws) == 0
+    assert ((outs[0] - outs[1]).abs() <= 2.0 ** -7 * outs[1].abs() + 2.0 ** -18 * 6).all()
