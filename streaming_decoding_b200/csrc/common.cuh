@@ -22,6 +22,15 @@ constexpr int kMaxWindow = 64;
 // next kernel start early in turn.  Under a plain launch both are no-ops.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Ends a kernel whose results the next one may read before its own
+// griddep_wait() (the attention over a bf16 cache brings in committed keys, page
+// ids and lengths that early, the keys by TMA): such a kernel does not call
+// griddep_launch(), so that the next one starts when all of its CTAs have ended,
+// and each of its writing threads calls this last.
+__device__ __forceinline__ void settle_writes() {
+    __threadfence();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,

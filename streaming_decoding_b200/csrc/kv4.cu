@@ -227,10 +227,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv4_append_kernel(const T* k, 
     }
 }
 
+// The kernel after this one does not start early: the rows may have been written
+// straight into pages of a bf16 cache, and the attention over those reads them before
+// its dependency wait.
 template <typename T, int U>
 __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(T* k, T* v, RowsParams p) {
     griddep_wait();
-    griddep_launch();
     const int lane = threadIdx.x & 31, u0 = blockIdx.y * (32 * U) + lane, units = p.hkv * 16;
     const uint32_t row = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
     if (row >= (uint32_t)p.rows) return;
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(T* k, T* v, Ro
         }
         store16((o.which ? v + row * p.v_stride : k + row * p.k_stride) + o.head * HD + o.blk * 16, x, p.wide);
     }
+    settle_writes();
 }
 
 // Four blocks of a lane (more loads in flight, one look-up for all) where a launch

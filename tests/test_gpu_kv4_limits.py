@@ -56,3 +56,32 @@ def test_more_pairs_than_there_are_tickets():
                                for x in (slice(i * m, (i + 1) * m) for i in range(parts))]).double())
         assert attention_error(ws) == 0
     assert ((outs[0] - outs[1]).abs() <= 2.0 ** -7 * outs[1].abs() + 2.0 ** -18 * 6).all()
+
+
+def test_rows_read_into_bf16_pages_are_there_for_the_attention_called_next():
+    """With one KV head, rows go straight into the pages of a bf16 cache, which the attention right behind reads."""
+    from streaming_decoding_b200 import attention_bf16, attention_workspace, kv4_append, kv4_pool, kv4_read
+    n_seq, pps, W = 4, 128, 16
+    pages, S = n_seq * pps, pps * 16 - W
+    four = kv4_pool(pages, 1)
+    err = i32([0])
+    per_page = dict(S=torch.zeros(pages, dtype=torch.int32, device="cuda"), n=torch.full((pages,), 16, dtype=torch.int32, device="cuda"))
+    ids = torch.randperm(pages, device="cuda").int()[:, None].contiguous()
+    pool = torch.zeros(pages + 1, 2, 1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    rows = pool.view(-1, 1, 128)
+    # row 32 b + r, r < 16: token r of page b's K; 16 rows on, its V
+    halves = rows[:32 * pages], rows[16:16 + 32 * pages]
+    table = torch.arange(pages, device="cuda").int().view(n_seq, pps)
+    Sd, nd = i32([S] * n_seq), i32([W] * n_seq)
+    q = torch.randn(n_seq * W, 4, 128, device="cuda").to(torch.bfloat16)
+    ws = attention_workspace(n_seq, W, 4, 1, pps * 16)
+    for i in range(20):
+        k, v = (torch.randn(16 * pages, 1, 128, device="cuda").to(torch.bfloat16) for _ in range(2))
+        kv4_append(k, v, four, ids, per_page["S"], per_page["n"], 16, err)
+        torch.cuda.synchronize()
+        kv4_read(four, ids, per_page["S"], per_page["n"], 32, err, out=halves)
+        first = attention_bf16(q, pool[:pages], table, Sd, nd, W, 4, 1, pps * 16, ws)
+        torch.cuda.synchronize()
+        again = attention_bf16(q, pool[:pages], table, Sd, nd, W, 4, 1, pps * 16, ws)
+        assert torch.equal(first, again), i
+    assert int(err) == 0 and first.float().abs().sum() > 0
