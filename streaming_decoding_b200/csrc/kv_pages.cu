@@ -13,7 +13,8 @@
 //
 // The kernels wait for the kernel before them before they read anything and
 // never let the kernel after them start early: kernels of the decode step read
-// page tables, lengths and cached keys before their own dependency wait.
+// page tables, lengths and cached keys (by TMA) before their own dependency wait
+// (settle_writes in common.cuh).
 //
 // A plan is a chain of dependent reads, each a trip to L2 (some 0.7 us) whatever
 // its size: its lists lie in shared memory where they fit, the first reference
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(wedlm_kv_pages
         for (int j = 0; j < kCopyVec; ++j)
             if (v0 + j * kCopyThreads < nvec) to[v0 + j * kCopyThreads] = v[j];
     }
-    __threadfence();
+    settle_writes();
 }
 
 // The copies by the plan's own CTA: the vectors of all pages in one row, so that
@@ -240,7 +241,7 @@ __device__ void move_alone(const wedlm_kv_pages& p, const PagesWs& w) {
         for (int j = 0; j < kCopyVec; ++j)
             if (to[j]) *to[j] = v[j];
     }
-    __threadfence();
+    settle_writes();
 }
 
 __global__ void __launch_bounds__(kPlanThreads) pages_copy_plan_kernel(const int32_t* src, const int32_t* dst, int n,
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve_kernel(const int32
             p.refs[page] = 1;
         }
     }
-    __threadfence();
+    settle_writes();
 }
 
 // Leaves in w.val[i] the full pages that child i is to share with its parent,
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(128) pages_free_kernel(const int32_t* seqs, we
         }
     }
     if (threadIdx.x == 0) p.S[q] = 0;
-    __threadfence();
+    settle_writes();
 }
 
 // Used pages move to the lowest ids: with u pages in use, the k-th used page at

@@ -1,0 +1,33 @@
+"""The page operations on the GPU beyond one call: what runs right behind them or beside their start."""
+import pytest
+
+from test_gpu_kv4 import i32
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("seqs", [1, 24])
+def test_copied_pages_are_there_for_the_attention_called_next(seqs):
+    """Pages of a bf16 cache copied (few by the plan itself, many by a kernel) and read by the attention behind it."""
+    from streaming_decoding_b200 import KVPages, attention_bf16, attention_workspace
+    hq, hkv, pps, W = 8, 2, 4 if seqs == 1 else 40, 16
+    m, S = seqs * pps, pps * 16 - W
+    pool = torch.zeros(1, 2 * m, 2, hkv, 16, 128, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(m, 2 * m, device="cuda").int().view(seqs, pps)
+    Sd, nd = i32([S] * seqs), i32([W] * seqs)
+    kp = KVPages(pool, table, Sd, torch.ones(2 * m, dtype=torch.int32, device="cuda"))
+    src, dst = torch.arange(m, device="cuda").int(), torch.arange(m, 2 * m, device="cuda").int()
+    assert (m * pool[0, 0].numel() * 2 <= 128 << 10) == (seqs == 1)  # both sides of the plan that copies alone
+    q = torch.randn(seqs * W, hq, 128, device="cuda").to(torch.bfloat16)
+    ws = attention_workspace(seqs, W, hq, hkv, pps * 16)
+    for i in range(20):
+        pool[0, :m].normal_()
+        torch.cuda.synchronize()
+        kp.copy(src, dst)
+        first = attention_bf16(q, pool[0], table, Sd, nd, W, hq, hkv, pps * 16, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(pool[0, :m], pool[0, m:])
+        again = attention_bf16(q, pool[0], table, Sd, nd, W, hq, hkv, pps * 16, ws)
+        assert torch.equal(first, again), i
+    assert kp.error() == 0 and first.float().abs().sum() > 0
