@@ -490,12 +490,11 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
     float sl[NT][2];
     int lim[NT][2], lim_min = ke - 1;
     const int64_t row0 = (int64_t)b * p.stride;
-    const float base = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int r = q0 + 8 * t + j8, rc = min(r, rows - 1);
         const int e = load_q(p.q + ((row0 + rc / g) * p.hq + h * g + rc % g) * HD + 32 * c, r < rows, qf[t]);
-        const float f = base * __int_as_float((127 - e) << 23);
+        const float f = score_factor(p.k_scale, e);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             sl[t][x] = __shfl_sync(0xffffffffu, f, (2 * c + x) * 4);

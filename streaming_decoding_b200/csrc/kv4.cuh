@@ -290,6 +290,16 @@ __device__ __forceinline__ bool item_next(ItemIter& it, const AttnKv4Params& p, 
     return false;
 }
 
+// What turns the product of a q row that was scaled by 2^e and a key without its scale into a
+// score in units of log2: kept inside fp32's normal range whatever the scale and e (a factor of
+// zero would turn a masked score, -inf, into NaN, an infinite one a score of zero).  Products
+// are below 2^34 and above 2^-34: with a factor of 2^-126 every score is as good as zero, and
+// with one of 2^89 two scores are equal or far apart, as with the true factors beyond.
+__device__ __forceinline__ float score_factor(float k_scale, int e) {
+    const float f = 1.4426950408889634f / sqrtf((float)HD) * k_scale * __int_as_float((127 - e) << 23);
+    return fminf(fmaxf(f, 0x1p-126f), 0x1p89f);
+}
+
 // What the outputs are multiplied by, given the weights' sum: 0 for a row that
 // saw no key (every page of it outside the pool), NaN where the sum is.
 __device__ __forceinline__ float out_factor(float v_scale, float l) { return l > 0.f || l != l ? v_scale / l : 0.f; }

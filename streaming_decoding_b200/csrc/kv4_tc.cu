@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                 ok = warp_wait(&q_full[0], li & 1, err);
                 ex = s_ex[lane_row];
             }
-            const float sl = 1.4426950408889634f / sqrtf((float)HD) * p.k_scale * __int_as_float((127 - ex) << 23);
+            const float sl = score_factor(p.k_scale, ex);
             const int lim = min(item.S + qr / g, item.ke - 1);               // last key the row sees
             const int all = min(item.S + item.q0 / g, item.ke - 1);          // last key every row of the tile sees
             const int ks = item.ks, nsplit = item.nsplit, sp = item.sp;

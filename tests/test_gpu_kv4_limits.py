@@ -1,12 +1,17 @@
-"""The 4-bit cache on the GPU beyond one call's sizes: workspaces that calls of other sizes have used."""
+"""The 4-bit cache on the GPU beyond one call and at the ends of what its entry points accept: workspaces that
+calls of other sizes have used, what runs right behind a call, scores outside fp32."""
 import numpy as np
 import pytest
 
 import _kv4_ref as R
-from test_gpu_kv4 import dev, i32
+from test_gpu_kv4 import attention_case, dev, i32
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
+
+# Rows of a window that take each kernel, with 4 query heads to a KV head: tiles
+# of 8, of 16, of 128 (its rows repeated) and of 256 query rows.
+STRIDES = [1, 4, 16, 80]
 
 
 def test_one_workspace_serves_calls_of_all_sizes():
@@ -85,3 +90,29 @@ def test_rows_read_into_bf16_pages_are_there_for_the_attention_called_next():
         again = attention_bf16(q, pool[:pages], table, Sd, nd, W, 4, 1, pps * 16, ws)
         assert torch.equal(first, again), i
     assert int(err) == 0 and first.float().abs().sum() > 0
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+@pytest.mark.parametrize("k_scale", [2.0 ** -59, 2.0 ** -30])
+def test_tiny_scores_weigh_all_keys_alike(stride, k_scale):
+    """The factor of the scores lies below fp32's range: masked keys still weigh nothing, the others alike."""
+    attention_case(31, 8, 2, stride, [300, 3], [stride, 1], qstd=2.0 ** -80, scales=(k_scale, 0.25))
+    attention_case(31, 8, 2, stride, [300, 3], [stride, 1], qstd=2.0 ** -120, scales=(k_scale, 0.25), max_ctx=60000)
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+def test_zero_keys_with_a_factor_beyond_fp32(stride):
+    """Scores of zero times a factor above fp32's range: the mean of the visible values."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    rng = np.random.default_rng(34)
+    table, pages = R.random_tables(rng, [(100 + stride + 15) // 16], 1)
+    pool = np.zeros((pages, 2, 2, R.HALF), np.uint8)
+    R.put(pool, table, 0, 0, 1, rng.standard_normal((100 + stride, 2, 128)), 1.0)
+    q = (torch.randn(stride, 8, 128) * 1e37).to(torch.bfloat16).cuda()
+    ws = attention_kv4_workspace(1, stride, 8, 2, 100 + stride)
+    out = attention_kv4(q, dev(pool), dev(table), i32([100]), i32([stride]), stride, 8, 2, 100 + stride, ws, 2.0 ** 58, 1.0)
+    V = R.get(pool, table, 0, 0, 100 + stride, 1, 1.0)
+    mean = np.cumsum(V, 0)[100:] / np.arange(101, 101 + stride)[:, None, None]
+    # half a step of the output and, of the fp32 sums of at most 180 values below 8, a step for each
+    off = np.abs(out.double().cpu().numpy() - np.repeat(mean, 4, 1))
+    assert (off <= 2.0 ** -8 * np.abs(np.repeat(mean, 4, 1)) + 180 * 2.0 ** -23 * 8).all() and attention_error(ws) == 0
