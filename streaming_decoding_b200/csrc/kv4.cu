@@ -366,7 +366,7 @@ __device__ __forceinline__ int load_q(const bf16* q, bool live, uint32_t (&a)[16
     for (int j = 0; j < 16; ++j) m = max(m, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int e = m ? min(100, 14 + 127 - (int)(m >> 7)) : 0;
+    const int e = min(100, 14 + 127 - (int)(m >> 7));
     const float f = __int_as_float((e + 127) << 23);
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -507,13 +507,14 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
 
     float o[8][NT][4] = {};
     // Per own column: the running maximum m of the scores in the exp2 domain and
-    // the weights' sum; a weight is exp2(score + z), z = 6 - m (huge before the
-    // first key, so that any visible key raises the maximum).
+    // the weights' sum; a weight is exp2(score + z), z = 6 - m (before the first key
+    // kNoMax).  The score is rounded before z is added, as m was: of a fused product and
+    // sum the part that m lost would remain, more than any exponent at scores past 2^28.
     float m[NT][2], z[NT][2], l[NT][2] = {};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         m[t][0] = m[t][1] = -INFINITY;
-        z[t][0] = z[t][1] = 1e30f;
+        z[t][0] = z[t][1] = kNoMax;
     }
     // A page's 16 keys.  (One body, its masks under a branch: the loop stays small
     // enough for the instruction cache.)
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                e[t][x] = fmaf(sc[t][x], sl[t][x & 1], z[t][x & 1]);
+                e[t][x] = __fadd_rn(__fmul_rn(sc[t][x], sl[t][x & 1]), z[t][x & 1]);
                 top = fmaxf(top, e[t][x]);
             }
         if (__any_sync(0xffffffffu, top > kWeightLog2 + kLazyLog2)) {
@@ -585,7 +586,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    float v = fmaxf(sc[t][x] * sl[t][x], sc[t][2 + x] * sl[t][x]);
+                    const float s0 = __fmul_rn(sc[t][x], sl[t][x]), s1 = __fmul_rn(sc[t][2 + x], sl[t][x]);
+                    float v = fmaxf(s0, s1);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
                     if (v > m[t][x]) {
@@ -599,8 +601,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
                             o[y][t][2 + x] *= f;
                         }
                     }
-                    e[t][x] = fmaf(sc[t][x], sl[t][x], z[t][x]);
-                    e[t][2 + x] = fmaf(sc[t][2 + x], sl[t][x], z[t][x]);
+                    e[t][x] = __fadd_rn(s0, z[t][x]);
+                    e[t][2 + x] = __fadd_rn(s1, z[t][x]);
                 }
         }
         uint32_t bt[NT][2];

@@ -98,6 +98,10 @@ __device__ __forceinline__ void st_global8(void* p, const uint32_t* r) {
 constexpr int kMaxSplits = 128;       // key chunks of a row tile
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum tolerated before O is rescaled
 constexpr float kWeightLog2 = 6.0f;   // weights are held times 2^6
+// In place of what a row adds to its scores before it has seen a key: any visible one (at
+// least -2^124, see score_factor) raises the maximum, a masked one (-inf) does not.
+constexpr float kNoMax = 0x1.8p127f;
+constexpr float kNearFactor = 0x1p-10f;  // score factor up to which scores are below 2^23.4 (q rows up to 128 at k_scale 1)
 
 struct AttnKv4Params {
     const bf16* q;

@@ -39,6 +39,7 @@
 //   1  bulk copies of the raw pages.
 // All waits are bounded; a timeout sets the device error word.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4.cuh"
 
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                     mx = max(mx, max(max(u.x & 0x7FFFu, (u.x >> 16) & 0x7FFFu), max(u.y & 0x7FFFu, (u.y >> 16) & 0x7FFFu)));
                     mx = max(mx, max(max(u.z & 0x7FFFu, (u.z >> 16) & 0x7FFFu), max(u.w & 0x7FFFu, (u.w >> 16) & 0x7FFFu)));
                 }
-                ex = mx ? min(100, 14 + 127 - (int)(mx >> 7)) : 0;
+                ex = min(100, 14 + 127 - (int)(mx >> 7));
                 const float f = __int_as_float((ex + 127) << 23);
                 auto scaled = [&](uint32_t w) {
                     return pack_half2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
@@ -584,8 +585,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             const int ks = item.ks, nsplit = item.nsplit, sp = item.sp;
             __syncwarp();
             if (lane == 0) bar_arrive(&item_empty[li % NITEM]);
-            float m = -INFINITY, z = 1e30f, l = 0.f;
+            // The running maximum m in units of log2 and the weights' sum l.  A weight is
+            // 2^(sl product + off), off = 6 - m, in one fma: m and off may be wrong by half a unit
+            // in their last place, so scores must stay below 2^23.4, as they do with a factor up
+            // to kNearFactor.  A row with a larger one has weights of 2^(sl (product + off) + 6),
+            // -off the largest product; a warp with such a row takes the loop with that sum (its
+            // other rows add 0 there).  That loop for all: 344 us for 326 at 64 windows of 32
+            // over 8k.
+            const bool far = sl > kNearFactor;
+            float m = -INFINITY, off = kNoMax, l = 0.f;
             bool any = false;  // O holds something
+            auto weigh_blocks = [&](auto far_rows) {  // the item's blocks of the tile
+            constexpr bool FAR = decltype(far_rows)::value;
             for (int j = ROWS ? 0 : t; j < nblk; j += ROWS ? 1 : 2, ++x) {
                 if (!(ok = warp_wait(&s_full[t], x & 1, err))) break;
                 tc_fence_after();
@@ -627,12 +638,12 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         take_max(rb);
                     }
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const bool grew = fmaf(top, sl, z) > kWeightLog2 + kLazyLog2;
+                    const bool grew = FAR && far ? top > -off : fmaf(top, sl, off) > kWeightLog2 + kLazyLog2;
                     if (__any_sync(0xffffffffu, grew)) {
                         const float v = top * sl, f = grew ? exp2_fast(m - v) : 1.f;
                         if (grew) {
                             m = v;
-                            z = kWeightLog2 - v;
+                            off = FAR && far ? -top : kWeightLog2 - v;
                             l *= f;
                         }
                         if (any) {
@@ -648,14 +659,18 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                         }
                     }
                     uint64_t sum[2] = {0, 0};
-                    const uint64_t sl2 = pair(sl, sl), z2 = pair(z, z);
+                    const float z = FAR && far ? kWeightLog2 : off, shift = FAR && far ? off : 0.f;
+                    const uint64_t sl2 = pair(sl, sl), z2 = pair(z, z), shift2 = pair(shift, shift);
                     // P of 32 keys over the first half of their own S: the arguments, then the
                     // exponentials, then the sums, so that the exp2 unit is fed without a pause
                     auto weigh = [&](int c, const uint32_t (&r)[32]) {
                         uint32_t pk[16];
                         float2 v[16];
 #pragma unroll
-                        for (int y = 0; y < 16; ++y) v[y] = unpair(fma2(pair(r[2 * y], r[2 * y + 1]), sl2, z2));
+                        for (int y = 0; y < 16; ++y) {
+                            const uint64_t s2 = pair(r[2 * y], r[2 * y + 1]);
+                            v[y] = unpair(fma2(FAR ? add2(s2, shift2) : s2, sl2, z2));
+                        }
 #pragma unroll
                         for (int y = 0; y < 16; ++y) v[y] = make_float2(exp2_fast(v[y].x), exp2_fast(v[y].y));
 #pragma unroll
@@ -687,6 +702,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                 __syncwarp();
                 if (lane == 0) bar_arrive(&p_full[t]);
             }
+            };
+            if (__any_sync(0xffffffffu, far)) weigh_blocks(std::true_type{});
+            else weigh_blocks(std::false_type{});
             base += nblk;
             if (ok && any) {
                 ok = warp_wait(&pv_done[t], (x - 1) & 1, err);

@@ -116,3 +116,47 @@ def test_zero_keys_with_a_factor_beyond_fp32(stride):
     # half a step of the output and, of the fp32 sums of at most 180 values below 8, a step for each
     off = np.abs(out.double().cpu().numpy() - np.repeat(mean, 4, 1))
     assert (off <= 2.0 ** -8 * np.abs(np.repeat(mean, 4, 1)) + 180 * 2.0 ** -23 * 8).all() and attention_error(ws) == 0
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+@pytest.mark.parametrize("qstd,k_scale", [(1e9, 1.0), (1e20, 1.0), (1e37, 1.0), (1e37, 2.0 ** 58), (1e-6, 2.0 ** 58)])
+@pytest.mark.parametrize("max_ctx", [None, 60000])
+def test_scores_of_any_size_pick_the_largest(stride, qstd, k_scale, max_ctx):
+    """Scores far beyond 2^24 and beyond fp32: the output is the value of the best key where that is clear.
+
+    A score is off by at most 2^-17 of T = sum |q k| (128 fp32 products and sums) and 2^-22 of itself (its
+    factor, its product). Two scores that differ by more than 2^-15 T keep their order and at least 2^-16 T of
+    their distance, in units of log2 at least 2^-16 T / sqrt(128) with T over 2^30: 2^10, which leaves
+    the lesser no weight at all. A value has 6 significant bits, so the output is it, exactly."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    rng = np.random.default_rng(32)
+    hq, hkv, S, n = 8, 2, [500, 30], [stride, min(stride, 3)]
+    table, pages = R.random_tables(rng, [(s + r + 15) // 16 for s, r in zip(S, n)], 1)
+    pool = np.zeros((pages, hkv, 2, R.HALF), np.uint8)
+    for b in range(2):
+        for which in range(2):
+            R.put(pool, table, b, 0, which, rng.standard_normal((S[b] + n[b], hkv, 128)), 1.0)
+    q = (torch.from_numpy(rng.standard_normal((2 * stride, hq, 128))) * qstd).to(torch.bfloat16)
+    ctx = max_ctx or 500 + stride
+    ws = attention_kv4_workspace(2, stride, hq, hkv, ctx)
+    out = attention_kv4(q.cuda(), dev(pool), dev(table), i32(S), i32(n), stride, hq, hkv, ctx, ws, k_scale, 0.25)
+    torch.cuda.synchronize()
+    assert attention_error(ws) == 0
+    out, qd = out.double().cpu().numpy(), q.double().numpy()
+    clear = total = 0
+    for b in range(2):
+        K, V = (R.get(pool, table, b, 0, S[b] + n[b], w, g) for w, g in ((0, k_scale), (1, 0.25)))
+        for r in range(n[b]):
+            for h in range(hq):
+                k = K[:S[b] + r + 1, h // 4]
+                z, T = k @ qd[b * stride + r, h], (np.abs(k) @ np.abs(qd[b * stride + r, h])).max()
+                assert T > 2.0 ** 30
+                two = np.sort(z)[-2:]
+                got = out[b * stride + r, h]
+                total += 1
+                if len(two) == 1 or two[1] - two[0] > 2.0 ** -15 * T:
+                    clear += 1
+                    assert np.array_equal(got, V[z.argmax(), h // 4])
+                else:
+                    assert np.isfinite(got).all()
+    assert clear > 0.9 * total
