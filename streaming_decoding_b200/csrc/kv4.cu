@@ -590,7 +590,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
                     float v = fmaxf(s0, s1);
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-                    if (v > m[t][x]) {
+                    // (by this row's own scores alone: no result depends on the rows beside it)
+                    if (__fadd_rn(v, z[t][x]) > kWeightLog2 + kLazyLog2) {
                         const float f = exp2_fast(m[t][x] - v);
                         m[t][x] = v;
                         z[t][x] = kWeightLog2 - v;

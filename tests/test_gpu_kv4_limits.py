@@ -160,3 +160,17 @@ def test_scores_of_any_size_pick_the_largest(stride, qstd, k_scale, max_ctx):
                 else:
                     assert np.isfinite(got).all()
     assert clear > 0.9 * total
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+def test_a_row_of_huge_scores_leaves_the_others_as_they_are(stride):
+    """Rows side by side in a warp keep their results, bit for bit, when one of them has scores past 2^30."""
+    from streaming_decoding_b200 import attention_kv4
+    args, good = attention_case(35, 8, 2, stride, [500, 70], [stride, max(1, stride // 2)])
+    q = args[0].clone()
+    q[0, 5] *= 2.0 ** 40
+    out = attention_kv4(q, *args[1:], out=torch.full_like(good, 7.0))
+    keep = torch.ones(good.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 5] = False
+    assert torch.equal(out[keep], good[keep]) and torch.isfinite(out[0, 5].float()).all()
+    assert not torch.equal(out[0, 5], good[0, 5])
