@@ -299,7 +299,11 @@ __device__ __forceinline__ bool item_next(ItemIter& it, const AttnKv4Params& p, 
 // zero would turn a masked score, -inf, into NaN, an infinite one a score of zero).  Products
 // are below 2^34 and above 2^-34: with a factor of 2^-126 every score is as good as zero, and
 // with one of 2^89 two scores are equal or far apart, as with the true factors beyond.
+// A row with an infinity or a NaN (its e) has NaN: the softmax of its scores is that, also
+// where all of them are -inf, which are not to be taken for masked ones.
+constexpr int kNotFinite = 14 + 127 - 255;
 __device__ __forceinline__ float score_factor(float k_scale, int e) {
+    if (e == kNotFinite) return __int_as_float(0x7FC00000);
     const float f = 1.4426950408889634f / sqrtf((float)HD) * k_scale * __int_as_float((127 - e) << 23);
     return fminf(fmaxf(f, 0x1p-126f), 0x1p89f);
 }

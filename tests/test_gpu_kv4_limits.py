@@ -174,3 +174,18 @@ def test_a_row_of_huge_scores_leaves_the_others_as_they_are(stride):
     keep[0, 5] = False
     assert torch.equal(out[keep], good[keep]) and torch.isfinite(out[0, 5].float()).all()
     assert not torch.equal(out[0, 5], good[0, 5])
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+def test_an_infinity_in_q_leaves_nan_whatever_its_sign(stride):
+    """Scores of an infinite q are infinities or NaN: their softmax is NaN, also where all of them are -inf."""
+    from streaming_decoding_b200 import attention_kv4
+    args, good = attention_case(33, 8, 2, stride, [0, 0], [1, min(stride, 2)])
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        q = args[0].clone()
+        q[0, 3, 17] = bad
+        q[stride, 6, 80] = -bad
+        out = attention_kv4(q, *args[1:], out=torch.full_like(good, 7.0))
+        hit = torch.zeros(good.shape[:2], dtype=torch.bool, device="cuda")
+        hit[0, 3] = hit[stride, 6] = True
+        assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
