@@ -531,8 +531,9 @@ wedlm_status wedlm_kv4_read(const void* kv4_pool, int32_t num_pages, int32_t n_k
  * bounded wait gave up).  The cache enters the products unrounded; q and the
  * softmax weights are rounded to 11 significant bits, sums are fp32.  Scores may be
  * of any size; a q row with a NaN or an infinity gives NaN, a row that sees no key
- * (all its pages left out) zeros.  Results do not depend on other sequences.  Asynchronous on `stream`; no allocation.  Calls
- * that may overlap need a workspace each. */
+ * (all its pages left out) zeros.  Results do not depend on other sequences.
+ * Asynchronous on `stream`; no allocation.  Calls that may overlap need a
+ * workspace each. */
 wedlm_status wedlm_attention_kv4_workspace_bytes(int32_t n_seq, int32_t stride, int32_t n_heads, int32_t n_kv_heads,
                                                  int32_t max_ctx, int64_t* bytes);
 wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t num_pages, int32_t n_heads,

@@ -447,10 +447,10 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
         return;
     }
     const int kend = S + (min(q0 + kRows, rows) - 1) / g + 1;
-    const int nsplit = (kend + p.chunk - 1) / p.chunk;
+    const int nsplit = (kend - 1) / p.chunk + 1;
     if (sp >= nsplit) return;
-    const int ke = min(kend, ks + p.chunk);
-    const int npages = (ke + kPage - 1) / kPage - page0, steps = (npages + kStep - 1) / kStep;
+    const int ke = ks + min(kend - ks, p.chunk);
+    const int npages = (ke - 1) / kPage + 1 - page0, steps = (npages + kStep - 1) / kStep;
     // Step k's pages into its stage; a page outside the pool is not loaded and
     // its keys count as masked.
     uint32_t gone = 0;  // bit kStep * s + x: page x of stage s is not there
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kMaxSplits) attn_kv4_join_kernel(const AttnKv4
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride), g = p.hq / p.hkv;
     if (r >= n || S < 0 || (int64_t)S + n > p.max_ctx) return;
     const int q_end = min(((r * g + head % g) / p.tile_rows + 1) * p.tile_rows, n * g);
-    const int nsplit = (S + (q_end - 1) / g + 1 + p.chunk - 1) / p.chunk;
+    const int nsplit = (S + (q_end - 1) / g) / p.chunk + 1;
     if (nsplit <= 1) return;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

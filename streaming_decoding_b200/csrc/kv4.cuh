@@ -170,7 +170,7 @@ __device__ __forceinline__ int group_load(const AttnKv4Params& p, int grp, int& 
         set_error(p.err, kErrBounds);
         return 0;
     }
-    return (S + (min(q0 + p.tile_rows, rows) - 1) / g + p.chunk) / p.chunk;
+    return (S + (min(q0 + p.tile_rows, rows) - 1) / g) / p.chunk + 1;
 }
 
 __device__ __forceinline__ void item_fill(const AttnKv4Params& p, int grp, int h, int sp, int S, int rows, Item& o) {
@@ -181,9 +181,9 @@ __device__ __forceinline__ void item_fill(const AttnKv4Params& p, int grp, int h
     o.S = S;
     o.rows = rows;
     const int kend = S + (min(o.q0 + p.tile_rows, rows) - 1) / (p.hq / p.hkv) + 1;
-    o.nsplit = (kend + p.chunk - 1) / p.chunk;
+    o.nsplit = (kend - 1) / p.chunk + 1;  // (positions, and ends of pages and blocks less one, fit 32 bits; sums past them may not)
     o.ks = sp * p.chunk;
-    o.ke = min(kend, o.ks + p.chunk);
+    o.ke = o.ks + min(kend - o.ks, p.chunk);
 }
 
 // Called by all threads of the CTA; synchronises it.

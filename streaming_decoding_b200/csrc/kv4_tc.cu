@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
             __syncwarp();
             if (!has) break;
             const int32_t* table = p.table + (int64_t)item.b * p.pages_per_seq;
-            const int page0 = item.ks / kPage, npages = (item.ke + kPage - 1) / kPage - page0;
+            const int page0 = item.ks / kPage, npages = (item.ke - 1) / kPage + 1 - page0;
             const int nblk = blocks_of(item);
             int ids = -1;
             for (int j = 0; j < nblk && ok; ++j, ++gb) {

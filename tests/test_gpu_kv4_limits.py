@@ -92,6 +92,24 @@ def test_rows_read_into_bf16_pages_are_there_for_the_attention_called_next():
     assert int(err) == 0 and first.float().abs().sum() > 0
 
 
+def softmax64(q, K, V, seen):
+    """(out, bound) of q [n, hq, 128] over keys K, V [keys, hkv, 128] where seen [n, keys], in 64 bits. The bound's
+    terms are those of test_gpu_kv4.reference; rows that see nothing are zero."""
+    n, hq, keys, g = len(q), q.shape[1], len(K), q.shape[1] // K.shape[1]
+    out, bound = np.zeros(q.shape), np.zeros(q.shape)
+    some = seen.any(1)
+    for h in range(hq):
+        k, v = K[:, h // g], V[:, h // g]
+        z = np.where(seen, q[:, h] @ k.T / np.sqrt(128), -np.inf)[some]
+        w = np.exp(z - z.max(-1, keepdims=True))
+        w /= w.sum(-1, keepdims=True)
+        out[some, h] = w @ v
+        T = (np.abs(q[some, h]) @ np.abs(k).T).max(-1) / np.sqrt(128)
+        share = 2.0 ** -11 + 2 * (2.0 ** -17 * T + 2.0 ** -21 * (1 + T)) + 2 * (keys / 16 + 8) * 2.0 ** -23
+        bound[some, h] = (share[:, None] * (w @ np.abs(v)) + keys * 2.0 ** -31 * np.abs(v).max()) * (1 + 2.0 ** -8)
+    return out, bound + 2.0 ** -8 * np.abs(out)
+
+
 @pytest.mark.parametrize("stride", STRIDES)
 @pytest.mark.parametrize("k_scale", [2.0 ** -59, 2.0 ** -30])
 def test_tiny_scores_weigh_all_keys_alike(stride, k_scale):
@@ -189,3 +207,28 @@ def test_an_infinity_in_q_leaves_nan_whatever_its_sign(stride):
         hit = torch.zeros(good.shape[:2], dtype=torch.bool, device="cuda")
         hit[0, 3] = hit[stride, 6] = True
         assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+def test_positions_up_to_the_last_of_32_bits(stride):
+    """A sequence that ends at position 2^31 - 2, nearly all of its pages left out: those that are there, at both ends
+    and around the middle, are seen where they lie."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    ctx = 2 ** 31 - 1
+    S, rng = ctx - stride, np.random.default_rng(36)
+    places = np.unique(np.concatenate([[0, 5], 2 ** 26 + np.arange(-2, 3), np.arange(2 ** 27 - 8, 2 ** 27)]))
+    pages = len(places)
+    codes, scales = R.encode(rng.standard_normal((pages, 1, 2, 16, 128)), 1.0)
+    raw = np.concatenate([codes.reshape(pages, 1, 2, -1), scales.reshape(pages, 1, 2, -1)], -1)
+    table = torch.full((1, 2 ** 27), -1, dtype=torch.int32, device="cuda")
+    table[0, dev(places)] = torch.arange(pages, device="cuda").int()
+    q = torch.from_numpy(rng.standard_normal((stride, 4, 128))).to(torch.bfloat16)
+    ws = attention_kv4_workspace(1, stride, 4, 1, ctx)
+    out = attention_kv4(q.cuda(), dev(raw), table, i32([S]), i32([stride]), stride, 4, 1, ctx, ws, 1.0, 0.25)
+    torch.cuda.synchronize()
+    assert attention_error(ws) == 1  # pages were left out
+    near = np.arange(pages, dtype=np.int32)[None]
+    K, V = (R.get(raw, near, 0, 0, 16 * pages, w, g) for w, g in ((0, 1.0), (1, 0.25)))
+    at = (places[:, None] * 16 + np.arange(16)).reshape(-1)
+    ref, bound = softmax64(q.double().numpy(), K, V, at[None] <= S + np.arange(stride)[:, None])
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
