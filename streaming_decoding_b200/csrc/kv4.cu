@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
             if (wanted && page[x] >= 0 && page[x] < p.num_pages) {
                 bytes += kHeadPage;
             } else {
-                if (wanted) set_error(p.err, kErrBounds);
+                if (wanted && lane == 0) set_error(p.err, kErrBounds);
                 gone |= 1u << (kStep * s + x);
                 page[x] = -1;
             }
