@@ -828,9 +828,9 @@ bool plan_attn_kv4(int n_seq, int stride, int hq, int hkv, int max_ctx, AttnKv4P
     return pairs * w->max_splits <= INT32_MAX && (int64_t)n_seq * stride * hq <= INT32_MAX;
 }
 
-bool power_of_two(float x) {
+bool valid_scale(float x) {
     int e;
-    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e > -60 && e < 60;
+    return std::isfinite(x) && x > 0.f && std::frexp(x, &e) == 0.5f && e >= -58 && e <= 59;  // 2^-59 to 2^58
 }
 
 wedlm_status rows_params(RowsParams* p, const void* k, const void* v, int32_t dtype, int64_t k_stride,
@@ -839,7 +839,7 @@ wedlm_status rows_params(RowsParams* p, const void* k, const void* v, int32_t dt
                          float k_scale, float v_scale, void* err) {
     if (n_seq < 0 || stride < 1 || hkv < 1 || num_pages < 1 || pages_per_seq < 1) return WEDLM_ERR_INVALID_ARG;
     if (dtype != WEDLM_DTYPE_F32 && dtype != WEDLM_DTYPE_BF16) return WEDLM_ERR_UNSUPPORTED;
-    if (!power_of_two(k_scale) || !power_of_two(v_scale)) return WEDLM_ERR_INVALID_ARG;
+    if (!valid_scale(k_scale) || !valid_scale(v_scale)) return WEDLM_ERR_INVALID_ARG;
     const int vec = dtype == WEDLM_DTYPE_F32 ? 4 : 8;
     if (k_stride < (int64_t)hkv * HD || v_stride < (int64_t)hkv * HD || k_stride % vec || v_stride % vec)
         return WEDLM_ERR_INVALID_ARG;
@@ -909,7 +909,7 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     if (!plan_attn_kv4(n_seq, stride, n_heads, n_kv_heads, max_ctx, &w)) return WEDLM_ERR_INVALID_ARG;
     if (!q || !kv4_pool || !page_table || !S || !n || !out || !workspace || num_pages < 1 || pages_per_seq < 1)
         return WEDLM_ERR_INVALID_ARG;
-    if (!power_of_two(k_scale) || !power_of_two(v_scale)) return WEDLM_ERR_INVALID_ARG;
+    if (!valid_scale(k_scale) || !valid_scale(v_scale)) return WEDLM_ERR_INVALID_ARG;
     if (workspace_bytes < (int64_t)w.bytes || ((uintptr_t)workspace & 255)) return WEDLM_ERR_INVALID_ARG;
     if ((((uintptr_t)q | (uintptr_t)kv4_pool) & 15) || ((uintptr_t)out & 31)) return WEDLM_ERR_INVALID_ARG;
     if (((uintptr_t)page_table | (uintptr_t)S | (uintptr_t)n) & 3) return WEDLM_ERR_INVALID_ARG;
