@@ -31,3 +31,27 @@ def test_copied_pages_are_there_for_the_attention_called_next(seqs):
         again = attention_bf16(q, pool[0], table, Sd, nd, W, hq, hkv, pps * 16, ws)
         assert torch.equal(first, again), i
     assert kp.error() == 0 and first.float().abs().sum() > 0
+
+
+def test_operations_on_another_stream_right_after_construction():
+    """The workspace that KVPages makes is zero before any stream can use it, however busy the stream that zeroes it is."""
+    from streaming_decoding_b200 import KVPages
+    from test_gpu_kv_pages import same, setup
+    other = torch.cuda.Stream()
+    for seed in range(3):
+        ref, kp = setup(seed, [40, 33, 100], 9, 40, 8)
+        parents, children = i32([0, 1, 2, 0]), i32([5, 6, 7, 8])
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)  # about 50 ms in front of what the current stream does next
+        kp = KVPages(kp.pool, kp.page_table, kp.S, kp.refs)
+        kp.fork(parents, children, stream=other)
+        kp.free(i32_on(other, [9]), stream=other)  # an error to be kept
+        ref.fork([0, 1, 2, 0], [5, 6, 7, 8])
+        ref.free([9])
+        same(ref, kp)
+        assert kp.error() == 1
+
+
+def i32_on(stream, values):
+    with torch.cuda.stream(stream):
+        return i32(values)
