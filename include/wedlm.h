@@ -548,7 +548,8 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
  *                pages of page_bytes (both multiples of 16, pool 16-byte
  *                aligned; layers must not overlap).
  *   page_table   int32 [n_seq][pages_per_seq]: a sequence's pages, -1 behind
- *                the last one (the table of wedlm_attention_bf16 / _kv4).
+ *                the last one (the table of wedlm_attention_bf16 / _kv4).  At
+ *                most 2^31 - 1 tokens a sequence and entries in all.
  *   S            int32 [n_seq]: committed tokens (0: an empty sequence).
  *   refs         int32 [num_pages], 16-byte aligned: sequences that hold the
  *                page; 0 = free. */

@@ -537,6 +537,8 @@ cudaError_t launch_move(const wedlm_kv_pages& p, const MoveArgs& a, int64_t most
 bool pages_ok(const wedlm_kv_pages* p, const void* ws, int64_t ws_bytes) {
     if (!p || !ws || !p->pool || !p->page_table || !p->S || !p->refs) return false;
     if (p->n_layers < 1 || p->num_pages < 1 || p->n_seq < 1 || p->pages_per_seq < 1) return false;
+    // positions and the table's entries (so the pages that one call can ask for, too) fit 32 bits
+    if (p->pages_per_seq > INT32_MAX / kPage || p->n_seq > INT32_MAX / p->pages_per_seq) return false;
     if (p->page_bytes < 16 || p->page_bytes % 16 || p->layer_stride % 16) return false;
     if (p->page_bytes > (INT64_MAX / 2) / p->num_pages) return false;
     if (p->n_layers > 1 && p->layer_stride < p->page_bytes * p->num_pages) return false;
