@@ -54,7 +54,12 @@ constexpr int RPP = 4;                        // pages of a raw stage (half a bl
 constexpr int RAW_BYTES = RPP * kHeadPage;
 constexpr int HALF_BYTES = KBLK * 128;        // 128 keys (or rows) x 64 dims of fp16
 constexpr int BUF_BYTES = 2 * HALF_BYTES;     // a widened K or V block, or a tile's Q
-constexpr int NRAW = 3;                       // raw stages
+constexpr int NRAW = 3;                       // raw stages: half block r lies in stage r % NRAW
+// Its barriers are numbers r % NRAWBAR.  An even number, so that a barrier belongs to
+// either the lower or the upper halves of blocks and the four warps that wait on it see
+// every one of its phases: with one to a stage they would see every other one, and a
+// parity cannot tell a phase from the one before last.
+constexpr int NRAWBAR = 4;
 constexpr int NBUF = 4;                       // widened K, V, K, V blocks
 constexpr int FLAGS = 8;                      // ring of per-block flags (more than any run-ahead)
 constexpr int NITEM = 4;                      // ring of items
@@ -71,12 +76,13 @@ constexpr int OFF_ITEMS = OFF_RAW + NRAW * RAW_BYTES;
 constexpr int OFF_ML = OFF_ITEMS + (int)sizeof(ItemTable);  // !ROWS: every softmax thread's (m, l)
 constexpr int OFF_EX = OFF_ML + 256 * 8;                    // !ROWS: the exponents added to Q's rows
 constexpr int OFF_BAR = OFF_EX + 128 * 4;
-constexpr int NBARS = 2 * NRAW + 2 * NBUF + 2 * NITEM + 8 + 1;
+constexpr int NBARS = 2 * NRAWBAR + 2 * NBUF + 2 * NITEM + 8 + 1;
 constexpr int OFF_FLAGS = OFF_BAR + NBARS * 8;
 constexpr int OFF_RING = OFF_FLAGS + FLAGS * 4;
 constexpr int SMEM = OFF_RING + NITEM * (int)sizeof(Item) + 16 + 1024 /* alignment */;
 static_assert(SMEM <= 227 * 1024, "shared memory");
 static_assert(NRAW / 2 + 4 < FLAGS, "flag ring");
+static_assert(NRAWBAR % 2 == 0 && NRAWBAR > NRAW, "raw barriers");
 static_assert(sizeof(ItemTable) % 8 == 0, "alignment of what follows");
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -256,9 +262,9 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
     ItemTable& items = *reinterpret_cast<ItemTable*>(smem + OFF_ITEMS);
     float2* s_ml = reinterpret_cast<float2*>(smem + OFF_ML);
     int* s_ex = reinterpret_cast<int*>(smem + OFF_EX);
-    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // [NRAW] a block's pages are there
-    uint64_t* raw_empty = raw_full + NRAW;                             // [NRAW] read (a warp a page)
-    uint64_t* buf_full = raw_empty + NRAW;                             // [NBUF] K or V widened (8 warps)
+    uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // [NRAWBAR] half a block's pages are there
+    uint64_t* raw_empty = raw_full + NRAWBAR;                          // [NRAWBAR] read (a warp a page)
+    uint64_t* buf_full = raw_empty + NRAWBAR;                          // [NBUF] K or V widened (8 warps)
     uint64_t* buf_empty = buf_full + NBUF;                             // [NBUF] its products done (of both tiles that it serves)
     uint64_t* q_full = buf_empty + NBUF;                               // [2] an item's Q is there (4 warps)
     uint64_t* s_full = q_full + 2;                                     // [2] S of a tile's block done
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NRAW; ++s) {
+        for (int s = 0; s < NRAWBAR; ++s) {
             mbar_init(&raw_full[s], 1);
             mbar_init(&raw_empty[s], RPP);
         }
@@ -360,20 +366,22 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
 #pragma unroll
                 for (int x = 0; x < 2; ++x, ++gr) {  // two stages to a block
                     const int s = gr % NRAW;
-                    if (!(ok = warp_wait(&raw_empty[s], ((gr / NRAW) & 1) ^ 1, err))) break;
+                    uint64_t* full = &raw_full[gr % NRAWBAR];
+                    const uint32_t old = gr - NRAW;  // the stage's last half block
+                    if (gr >= NRAW && !(ok = warp_wait(&raw_empty[old % NRAWBAR], (old / NRAWBAR) & 1, err))) break;
                     const uint32_t part = (have >> (RPP * x)) & ((1u << RPP) - 1);
-                    if (lane == 0) bar_expect(&raw_full[s], __popc(part) * kHeadPage);
+                    if (lane == 0) bar_expect(full, __popc(part) * kHeadPage);
                     __syncwarp();
                     if (there && lane < PPB && lane / RPP == x)
                         load_page(raw + s * RAW_BYTES + (lane % RPP) * kHeadPage,
-                                  p.pool + ((int64_t)page * p.hkv + item.h) * kHeadPage, &raw_full[s]);
+                                  p.pool + ((int64_t)page * p.hkv + item.h) * kHeadPage, full);
                 }
             }
         }
         // copies still in flight (only after an error) land before the CTA exits
         if (lane == 0)
             for (uint32_t j = gr > (uint32_t)NRAW ? gr - NRAW : 0u; j < gr; ++j)
-                mbar_wait_bounded(smem_u32(&raw_full[j % NRAW]), (j / NRAW) & 1, nullptr, 200000000LL);
+                mbar_wait_bounded(smem_u32(&raw_full[j % NRAWBAR]), (j / NRAWBAR) & 1, nullptr, 200000000LL);
     } else if (warp == WARP_MMA) {
         // -------------------------------------------------------------- MMA
         if (lane == 0) {
@@ -475,7 +483,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                     const uint32_t dst = place + (x % NBUF) * BUF_BYTES;
                     if (!(ok = warp_wait(&buf_empty[x % NBUF], ((x / NBUF) & 1) ^ 1, err))) break;
                     const uint32_t r = 2 * gb + w / RPP;
-                    if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAW], (r / NRAW) & 1, err))) break;
+                    if (kv == 0 && !(ok = warp_wait(&raw_full[r % NRAWBAR], (r / NRAWBAR) & 1, err))) break;
                     const uint8_t* src = raw + (r % NRAW) * RAW_BYTES + (w % RPP) * kHeadPage + kv * kHalfPage;
                     uint2 code[4];
                     uint32_t scale[4];
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1) attn_kv4_tc_kernel(const AttnKv4Pa
                                 if (4 * i + tok >= live) scale[i] = 0;
                         }
                         __syncwarp();
-                        if (lane == 0) bar_arrive(&raw_empty[r % NRAW]);  // (K and V of the page have been read)
+                        if (lane == 0) bar_arrive(&raw_empty[r % NRAWBAR]);  // (K and V of the page have been read)
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {

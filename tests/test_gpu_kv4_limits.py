@@ -232,3 +232,31 @@ def test_positions_up_to_the_last_of_32_bits(stride):
     at = (places[:, None] * 16 + np.arange(16)).reshape(-1)
     ref, bound = softmax64(q.double().numpy(), K, V, at[None] <= S + np.arange(stride)[:, None])
     assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+@pytest.mark.parametrize("there", ["lower half", "upper half", "some"])
+def test_blocks_that_lack_pages_keep_in_step(stride, there):
+    """Pages left out all along a sequence, so that one half of a 128-key block is there long before the other:
+    the keys that remain, and the same result each time."""
+    from streaming_decoding_b200 import attention_error, attention_kv4, attention_kv4_workspace
+    rng = np.random.default_rng(37)
+    pages, ctx = 250, 4000
+    S = ctx - stride
+    keep = {"lower half": np.arange(pages) % 8 < 4, "upper half": np.arange(pages) % 8 >= 4, "some": rng.random(pages) < 0.4}[there]
+    codes, scales = R.encode(rng.standard_normal((pages, 2, 2, 16, 128)), 1.0)
+    raw = np.concatenate([codes.reshape(pages, 2, 2, -1), scales.reshape(pages, 2, 2, -1)], -1)
+    order = rng.permutation(pages).astype(np.int32)
+    pool = np.empty_like(raw)
+    pool[order] = raw
+    table = np.where(keep, order, -1).astype(np.int32)[None]
+    q = torch.from_numpy(rng.standard_normal((stride, 8, 128))).to(torch.bfloat16)
+    args = (q.cuda(), dev(pool), dev(table), i32([S]), i32([stride]), stride, 8, 2, ctx)
+    ws = attention_kv4_workspace(*(1, stride, 8, 2, ctx))
+    outs = [attention_kv4(*args, ws, 1.0, 0.25) for _ in range(20)]
+    assert attention_error(ws) == 1 and all(torch.equal(o, outs[0]) for o in outs)
+    near = np.arange(pages, dtype=np.int32)[None]
+    K, V = (R.get(raw, near, 0, 0, 16 * pages, w, g) for w, g in ((0, 1.0), (1, 0.25)))
+    at = np.arange(16 * pages)
+    ref, bound = softmax64(q.double().numpy(), K, V, np.repeat(keep, 16)[None] & (at[None] <= S + np.arange(stride)[:, None]))
+    assert (np.abs(outs[0].double().cpu().numpy() - ref) <= bound).all()
