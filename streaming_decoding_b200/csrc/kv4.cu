@@ -296,11 +296,11 @@ cudaError_t launch_read(const RowsParams& p, void* k, void* v, cudaStream_t st) 
 // Attention over the 4-bit cache: out = softmax(q K^T / sqrt(128)) V of window
 // rows r over cache positions 0 .. S + r, as wedlm_attention_bf16.
 //
-// Work item (a CTA of one warp): NT * 8 query rows (window rows x the g heads
-// that share a KV head), one KV head, one chunk of keys, two pages at a time
-// through a ring of page buffers filled by bulk copies.  Codes go from shared memory
-// to registers, are widened and scaled there and feed mma.sync directly: no
-// widened copy of K or V is ever written anywhere.  The cache is the M side of
+// Work item (a CTA of one warp): all of a sequence's query rows of one KV head
+// (window rows x the g heads that share it, at most NT * 8), one chunk of keys, two
+// pages at a time through a ring of page buffers filled by bulk copies.  Codes go
+// from shared memory to registers, are widened and scaled there and feed mma.sync
+// directly: no widened copy of K or V is ever written anywhere.  The cache is the M side of
 // both products (S^T = K Q^T, O^T = V^T P^T), so that a token's 4 to 8 query
 // rows fill the 8-wide N side; P^T is S^T transposed in registers.  The dims
 // are permuted inside the products (which changes no sum): in K Q^T the lanes
@@ -414,7 +414,6 @@ __device__ __forceinline__ void join_range(const AttnKv4Params& p, int64_t at, i
 
 template <int NT>
 __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const AttnKv4Params p) {
-    constexpr int kRows = 8 * NT;
     __shared__ __align__(128) uint8_t ring[kStages][kStep][kHeadPage];
     __shared__ __align__(8) uint64_t bars[kStages];
     griddep_wait();
@@ -423,12 +422,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
     const int g = p.hq / p.hkv;
     // All sequences' first chunks, then their second ones, ...: items beyond a
     // sequence's end come last (chunks of a sequence in a row: 97 us for 94).
-    int64_t id = blockIdx.x;
-    const int tile = (int)(id % p.tiles);
-    id /= p.tiles;
-    const int h = (int)(id % p.hkv);
-    id /= p.hkv;
-    const int b = (int)(id % p.n_seq), sp = (int)(id / p.n_seq);
+    const unsigned pair = blockIdx.x / p.hkv;
+    const int h = (int)(blockIdx.x - pair * p.hkv), b = (int)(pair % p.n_seq), sp = (int)(pair / p.n_seq);
     const int S = __ldcg(p.S + b), n = min(__ldcg(p.n + b), p.stride);
     const int32_t* table = p.table + (int64_t)b * p.pages_per_seq;
     const int ks = sp * p.chunk, page0 = ks / kPage;
@@ -440,13 +435,13 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
-    const int rows = n * g, q0 = tile * kRows;
-    if (n <= 0 || q0 >= rows) return;
+    const int rows = n * g;  // at most 8 NT
+    if (n <= 0) return;
     if (S < 0 || (int64_t)S + n > p.max_ctx) {
         set_error(p.err, kErrBounds);
         return;
     }
-    const int kend = S + (min(q0 + kRows, rows) - 1) / g + 1;
+    const int kend = S + n;
     const int nsplit = (kend - 1) / p.chunk + 1;
     if (sp >= nsplit) return;
     const int ke = ks + min(kend - ks, p.chunk);
@@ -492,13 +487,13 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
     const int64_t row0 = (int64_t)b * p.stride;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        const int r = q0 + 8 * t + j8, rc = min(r, rows - 1);
+        const int r = 8 * t + j8, rc = min(r, rows - 1);
         const int e = load_q(p.q + ((row0 + rc / g) * p.hq + h * g + rc % g) * HD + 32 * c, r < rows, qf[t]);
         const float f = score_factor(p.k_scale, e);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             sl[t][x] = __shfl_sync(0xffffffffu, f, (2 * c + x) * 4);
-            lim[t][x] = min(S + min(q0 + 8 * t + 2 * c + x, rows - 1) / g, ke - 1);
+            lim[t][x] = min(S + min(8 * t + 2 * c + x, rows - 1) / g, ke - 1);
             lim_min = min(lim_min, lim[t][x]);
         }
     }
@@ -663,7 +658,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) l[t][x] += __shfl_xor_sync(0xffffffffu, l[t][x], d);
             // dims 16 j8 .. + 15 of the column's row
-            const int qr = q0 + 8 * t + 2 * c + x;
+            const int qr = 8 * t + 2 * c + x;
             if (qr >= rows) continue;
             const int64_t at = (row0 + qr / g) * p.hq + h * g + qr % g;
             if (nsplit == 1) {
@@ -687,14 +682,14 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
     __syncwarp();
     unsigned last = 0;
     if (lane == 0)
-        last = atomicInc(p.tickets + ((int64_t)b * p.hkv + h) * p.tiles + tile, nsplit - 1) == (unsigned)nsplit - 1;
+        last = atomicInc(p.tickets + (int64_t)b * p.hkv + h, nsplit - 1) == (unsigned)nsplit - 1;
     if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
     // Eight lanes a row, four rows at a time: lane x of the eight holds chunk x's
     // (m, l) and 16 of the dims.
-    const int x8 = lane & 7, end = min(q0 + kRows, rows);
-    for (int r0 = q0; r0 < end; r0 += 4) {
-        const int r = min(r0 + (lane >> 3), end - 1);
+    const int x8 = lane & 7;
+    for (int r0 = 0; r0 < rows; r0 += 4) {
+        const int r = min(r0 + (lane >> 3), rows - 1);
         const int64_t at = (row0 + r / g) * p.hq + h * g + r % g;
         const float2 ml = x8 < nsplit ? __ldcg(p.part_ml + at * p.max_splits + x8) : make_float2(-INFINITY, 0.f);
         const float4* po = reinterpret_cast<const float4*>(p.part_o + at * p.max_splits * HD) + x8;
@@ -718,7 +713,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 20 : 10) attn_kv4_kernel(const A
                 acc[d].w += f * v.w;
             }
         }
-        if (r0 + (lane >> 3) < end) {
+        if (r0 + (lane >> 3) < rows) {
 #pragma unroll
             for (int d = 0; d < 4; ++d) store_out(p, at, x8 + 8 * d, acc[d], out_factor(p.v_scale, ll));
         }

@@ -112,7 +112,7 @@ struct AttnKv4Params {
     bf16* out;
     float* part_o;       // [rows][hq][max_splits][128]
     float2* part_ml;     // [rows][hq][max_splits]
-    unsigned* tickets;   // [n_seq][hkv][tiles], zero between calls; nullptr: a second kernel joins the chunks
+    unsigned* tickets;   // [n_seq][hkv] (one tile a sequence), zero between calls; nullptr: a second kernel joins the chunks
     int* err;
     int num_pages, hq, hkv, pages_per_seq, n_seq, stride, max_ctx, chunk, max_splits;
     int tile_rows, tiles;  // query rows (window rows x heads of a KV head) of a tile, tiles of a sequence
