@@ -260,3 +260,53 @@ def test_blocks_that_lack_pages_keep_in_step(stride, there):
     at = np.arange(16 * pages)
     ref, bound = softmax64(q.double().numpy(), K, V, np.repeat(keep, 16)[None] & (at[None] <= S + np.arange(stride)[:, None]))
     assert (np.abs(outs[0].double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+@pytest.mark.parametrize("max_ctx", [None, 60000])
+def test_bad_pages_and_lengths_on_every_kernel(stride, max_ctx):
+    """A page id outside the pool: its keys are left out, nothing else changes; a length past the capacity or below
+    zero: the sequence is skipped. With whole and divided keys."""
+    from streaming_decoding_b200 import attention_error, attention_kv4
+    (q, pool, table, S, n, _, hq, hkv, ctx, ws, kg, vg), good = attention_case(38, 8, 2, stride, [700, 10, 300], [stride] * 3,
+                                                                               max_ctx=max_ctx)
+    call = lambda t, lengths: attention_kv4(q, pool, t, lengths, n, stride, hq, hkv, ctx, ws, kg, vg,  # noqa: E731
+                                            out=torch.full_like(good, 7.0))
+    raw, near, qd = pool.cpu().numpy(), table.cpu().numpy(), q.double().cpu().numpy()
+    for b, at in ((0, 0), (0, 17), (1, 0), (2, (300 + stride - 1) // 16)):
+        for bad in (-1, pool.shape[0], 2 ** 31 - 1, -2 ** 31):
+            t = table.clone()
+            t[b, at] = bad
+            ws[:4] = 0
+            out = call(t, S)
+            torch.cuda.synchronize()
+            assert attention_error(ws) == 1
+            mine = slice(b * stride, (b + 1) * stride)
+            rest = torch.ones(len(good), dtype=torch.bool, device="cuda")
+            rest[mine] = False
+            assert torch.equal(out[rest], good[rest])
+            keys = int(S[b]) + stride
+            K, V = (R.get(raw, near, b, 0, keys, w, g) for w, g in ((0, kg), (1, vg)))
+            pos = np.arange(keys)
+            seen = (pos[None] <= int(S[b]) + np.arange(stride)[:, None]) & (pos // 16 != at)[None]
+            ref, bound = softmax64(qd[mine], K, V, seen)
+            assert (np.abs(out[mine].double().cpu().numpy() - ref) <= bound).all()
+    for bad in (-1, ctx - stride + 1, 2 ** 31 - 1, -2 ** 31):
+        ws[:4] = 0
+        out = call(table, i32([700, bad, 300]))
+        torch.cuda.synchronize()
+        assert attention_error(ws) == 1 and (out[stride:2 * stride] == 7).all()
+        assert torch.equal(out[:stride], good[:stride]) and torch.equal(out[2 * stride:], good[2 * stride:])
+
+
+@pytest.mark.parametrize("stride", STRIDES)
+def test_nan_in_a_row_stays_there_on_every_kernel(stride):
+    from streaming_decoding_b200 import attention_kv4
+    args, good = attention_case(39, 8, 2, stride, [500, 40], [stride, stride])
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        q = args[0].clone()
+        q[0, 5, 17] = q[2 * stride - 1, 2, 127] = bad
+        out = attention_kv4(q, *args[1:])
+        hit = torch.zeros(good.shape[:2], dtype=torch.bool, device="cuda")
+        hit[0, 5] = hit[2 * stride - 1, 2] = True
+        assert out[hit].isnan().all() and torch.equal(out[~hit], good[~hit])
