@@ -34,7 +34,7 @@ constexpr int kPlanShared = 2048;  // entries of a list that a plan keeps in sha
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 4;  // 16-byte vectors per thread in flight
 constexpr int kShareRun = 128;  // pages that a warp shares at a time
-constexpr int64_t kAloneBytes = 128 << 10;  // what the plan of a copy moves by itself
+constexpr int64_t kAloneBytes = 64 << 10;  // what the plan of a copy moves by itself
 
 // Workspace: [0] the error word, [1] the number of planned copies, then the
 // copies (source, destination), one int per page (free pages, marks or the
@@ -569,9 +569,9 @@ wedlm_status wedlm_kv_pages_copy(const wedlm_kv_pages* pages, const int32_t* src
     if (!src || !dst) return WEDLM_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
     const PagesWs w = pages_ws(workspace, pages->num_pages, pages->n_seq);
-    // Little is copied by the plan itself: at three pages of 8 KB in two layers a call
-    // takes 5.4 us instead of 7.9 (in a captured graph, where a launch costs less,
-    // 5.4 and 4.6).
+    // Little is copied by the plan itself, which saves a launch: us eagerly (in a captured
+    // graph) for 16 KB 4.9 (4.1), with a second kernel 7.1 (4.9); 48 KB 5.1 (4.9) and 7.3
+    // (4.5); 64 KB 6.0 (5.9) and 7.1 (4.7); 128 KB 8.0 (7.9) and 7.2 (4.8).
     const bool alone = pages->page_bytes <= kAloneBytes && n <= kAloneBytes / pages->page_bytes / pages->n_layers;
     cudaError_t e = launch_pdl(pages_copy_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, src, dst, n, *pages, alone, w);
     if (e == cudaSuccess && !alone)

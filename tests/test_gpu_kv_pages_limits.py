@@ -18,7 +18,7 @@ def test_copied_pages_are_there_for_the_attention_called_next(seqs):
     Sd, nd = i32([S] * seqs), i32([W] * seqs)
     kp = KVPages(pool, table, Sd, torch.ones(2 * m, dtype=torch.int32, device="cuda"))
     src, dst = torch.arange(m, device="cuda").int(), torch.arange(m, 2 * m, device="cuda").int()
-    assert (m * pool[0, 0].numel() * 2 <= 128 << 10) == (seqs == 1)  # both sides of the plan that copies alone
+    assert (m * pool[0, 0].numel() * 2 <= 64 << 10) == (seqs == 1)  # both sides of the plan that copies alone
     q = torch.randn(seqs * W, hq, 128, device="cuda").to(torch.bfloat16)
     ws = attention_workspace(seqs, W, hq, hkv, pps * 16)
     for i in range(20):
@@ -55,3 +55,15 @@ def test_operations_on_another_stream_right_after_construction():
 def i32_on(stream, values):
     with torch.cuda.stream(stream):
         return i32(values)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3])
+def test_copies_around_what_the_plan_does_by_itself(n):
+    """64 KB in all (16 KB pages in two layers) is the most that the plan copies, more goes to a kernel."""
+    from test_gpu_kv_pages import same, setup
+    ref, kp = setup(11, [40], 2, 100, 6, 2, (2, 2, 16, 64))
+    src, dst = list(range(n)), list(range(50, 50 + n))
+    ref.copy(src, dst)
+    kp.copy(i32(src), i32(dst))
+    same(ref, kp)
+    assert ref.error == 0
