@@ -64,7 +64,7 @@ __device__ __forceinline__ uint8_t* half_page(const RowsParams& p, int page, con
 }
 
 // 32 bytes of a row, a whole memory sector: in one access where the rows allow it
-// (two of 16 bytes ask for the sector twice: 46 against 41 us at 16 x 1024 rows of
+// (two of 16 bytes ask for the sector twice: 5 us more of 41 at 16 x 1024 rows of
 // 8 heads, in and back out).
 __device__ __forceinline__ void load32(uint4* w, const void* x, int wide) {
     if (wide) {
@@ -273,9 +273,10 @@ __global__ void __launch_bounds__(32 * kRowWarps) kv4_read_kernel(T* k, T* v, Ro
 
 // Four blocks of a lane (more loads in flight, one look-up for all) where a launch
 // has rows enough to fill the GPU with that, else one (more warps).  In and back
-// out, 8 heads: 16 x 1024 bf16 rows 38 us with four, 60 with one (158 MB at 6.5 TB/s:
+// out, 8 heads: 16 x 1024 bf16 rows 43 us with four, 66 with one (158 MB at 6.5 TB/s:
 // 24 us; bound by the instructions of the conversions and by the latency of the
-// look-up); 16 x 16 fp32 rows 5.4 us with one, 8.6 with four (latency alone).
+// look-up), fp32 rows 71 and 76 (306 MB, 47 us; append alone 42 and 38); with one head
+// 15.5 and 14.9.  16 x 16 fp32 rows 5.7 us with one, 7.9 with four (latency alone).
 template <typename T>
 cudaError_t launch_append(const RowsParams& p, const void* k, const void* v, cudaStream_t st) {
     const unsigned ctas = (unsigned)((p.rows + kRowWarps - 1) / kRowWarps), per = (unsigned)(p.hkv + 1) / 2;
@@ -317,10 +318,11 @@ cudaError_t launch_read(const RowsParams& p, void* k, void* v, cudaStream_t st) 
 // outputs are fp32.
 //
 // Measured: 64 sequences of 1k to 8.2k keys, one row of 32 heads over 8 KV heads:
-// 94 us, 3.6 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
+// 92.6 us, 3.6 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
 // shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 65 %
 // busy: of the 20 warps that an SM's registers allow 15 are there on average, the
-// others end, start, or have no item left.  1 sequence of 256: 8.3 us, latency.
+// others end, start, or have no item left.  1 sequence of 256: 7.9 us, latency (the
+// four warps of a CTA, which joined through shared memory, 6.2; they lost at length).
 constexpr int kStep = 2;              // pages of a stage
 constexpr int kStages = 2;            // (three, at 16 warps an SM: slower)
 constexpr int kItemsPerSm = 48;       // (36 and 64: no faster)

@@ -24,9 +24,10 @@
 // thread's own chain of products and commits); 16 softmax warps, which share the
 // same schedulers, were no faster, an MMA thread for each tile slower (456 us:
 // products of both tiles alternate in the pipe).
-//   64 sequences at 8.2k to 8.7k, windows of 32, 7 heads to a KV head: 331 us,
-//   586 TFLOP/s (mma.sync items of 16 rows: 1180); 16 sequences of 128 to 2047,
-//   windows of 16, 4 heads: 30 us (51), of which the start takes 5 and the end 3.
+//   64 sequences at 8.2k to 8.7k, windows of 32, 7 heads to a KV head: 323 us,
+//   600 TFLOP/s (mma.sync items of 16 rows: 1180); 16 sequences of 128 to 2047,
+//   windows of 16, 4 heads: 31 us (51), of which the start takes 5 and the end 3;
+//   16 prompts of 512 rows 99 us, 64 of 1024 1.04 ms (32 and 8 heads).
 //
 // Persistent, one CTA to an SM.  Warps:
 //   8  softmax: thread i of tile t owns lane i of TMEM, a query row: Q to shared
