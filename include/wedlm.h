@@ -578,17 +578,19 @@ typedef struct wedlm_kv_pages {
  * copy     page dst[i] := page src[i] in every layer.  A page may be written by
  *          one entry only and not be read by another: the entries that write a
  *          page listed twice in dst, or listed in src too, are skipped (1).
- *          n <= num_pages.
+ *          (Entries with an id outside [0, num_pages) are skipped and stand in
+ *          no other entry's way.)  n <= num_pages.
  * reserve  sequence seqs[i] gets free pages behind its own until it has room for
  *          tokens[i] tokens (nothing happens where it has).  Rules: seqs distinct
  *          and in range, 0 <= tokens <= 16 * pages_per_seq, no -1 in front of a
  *          sequence's last page.  n <= n_seq.
- * fork     children[i], an empty sequence, becomes a copy of parents[i]: it
+ * fork     children[i], a sequence without pages, becomes a copy of parents[i]: it
  *          shares the parent's full pages and gets a free page with a copy of
  *          the last one if that is not full, so that both can be continued.
  *          (The parent's pages beyond its S tokens are not shared.)  Rules:
- *          children distinct, empty and not among the parents, the pages of the
- *          parent's S tokens present and in use.  n <= n_seq.
+ *          children distinct, without pages (rows of -1) and not among the
+ *          parents, the pages of the parent's S tokens present and in use.
+ *          n <= n_seq.
  * free     the sequence's pages lose a reference, its row becomes -1 and S 0.
  *          Listing one twice, or an empty one, is allowed.  n <= n_seq.
  * compact  moves pages so that the u pages in use are pages 0 .. u - 1: the k-th

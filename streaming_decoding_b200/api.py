@@ -603,7 +603,7 @@ class KVPages:
         self._call("wedlm_kv_pages_reserve", stream, seqs.data_ptr(), tokens.data_ptr(), n)
 
     def fork(self, parents, children, stream=None):
-        """children[i], an empty sequence, becomes a copy of parents[i] that shares its full pages."""
+        """children[i], a sequence without pages, becomes a copy of parents[i] that shares its full pages."""
         n = self._list(parents, "parents")
         self._list(children, "children", n)
         self._call("wedlm_kv_pages_fork", stream, parents.data_ptr(), children.data_ptr(), n)
