@@ -570,7 +570,7 @@ class KVPages:
                "wedlm_kv_pages_workspace_bytes")
         if workspace is None:
             workspace = torch.zeros(int(nb.value), dtype=torch.uint8, device=index)
-            # (the operations may come on any stream, and a caller does not see this memory: it is zero from here on)
+            # (operations may come on any stream, and a caller does not see this memory: it is zero from here on)
             if not torch.cuda.is_current_stream_capturing():
                 torch.cuda.current_stream(index).synchronize()
         _on(workspace, index, torch.uint8, workspace.shape, "workspace")

@@ -319,7 +319,7 @@ cudaError_t launch_read(const RowsParams& p, void* k, void* v, cudaStream_t st) 
 //
 // Measured: 64 sequences of 1k to 8.2k keys, one row of 32 heads over 8 KV heads:
 // 92.6 us, 3.6 TB/s, with the join's 9 (four warps to a CTA that joined their parts in
-// shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 65 %
+// shared memory: 132).  Bound by instructions, 373 a page, with the issue slots 67 %
 // busy: of the 20 warps that an SM's registers allow 15 are there on average, the
 // others end, start, or have no item left.  1 sequence of 256: 7.9 us, latency (the
 // four warps of a CTA, which joined through shared memory, 6.2; they lost at length).
@@ -913,9 +913,10 @@ wedlm_status wedlm_attention_kv4(const void* q, const void* kv4_pool, int32_t nu
     char* ws = static_cast<char*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;
     const AttnKv4Params p{(const bf16*)q, (const uint8_t*)kv4_pool, page_table, S, n, (bf16*)out,
-                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml), w.ticketed ? (unsigned*)(ws + w.off_ticket) : nullptr, (int*)ws,
-                          num_pages, n_heads, n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits,
-                          w.tile_rows, w.tiles, k_scale, v_scale};
+                          (float*)(ws + w.off_o), (float2*)(ws + w.off_ml),
+                          w.ticketed ? (unsigned*)(ws + w.off_ticket) : nullptr, (int*)ws, num_pages, n_heads,
+                          n_kv_heads, pages_per_seq, n_seq, stride, max_ctx, w.chunk, w.max_splits, w.tile_rows,
+                          w.tiles, k_scale, v_scale};
     const bool tc = w.tile_rows > 16;
     const dim3 grid((unsigned)((int64_t)n_seq * n_kv_heads * w.tiles * w.max_splits));
     cudaError_t e = tc                  ? launch_attn_kv4_tc(p, w.sms, st)
